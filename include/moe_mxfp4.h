@@ -71,8 +71,11 @@ typedef enum {
                                         (0x7f / 0xff), was decoded                  */
 #define MOE_DEVERR_TIMEOUT 0x4       /* a bounded pipeline wait gave up              */
 #define MOE_DEVERR_BAD_LOGIT 0x8     /* a token had fewer than k non-NaN router logits */
-#define MOE_DEVERR_OUT_OF_BOUNDS 0x10 /* bounds-checked builds only: an index fell
-                                        outside its buffer (the access was skipped) */
+#define MOE_DEVERR_OUT_OF_BOUNDS 0x10 /* an index fell outside its buffer and the access was
+                                        skipped: in every build a pair_rows entry >= R of
+                                        moe_dispatch_rows, moe_combine_rows and their
+                                        backward calls, in bounds-checked builds any
+                                        data-dependent index                            */
 
 /* moe_mxfp4_forward_ex flags */
 #define MOE_FLAG_WEIGHT_ON_INPUT 0x1u /* router weight scales each expert's input  */
@@ -330,6 +333,117 @@ int moe_mxfp4_expert_rows(const uint16_t *x_rows, int64_t R, int64_t H, int64_t 
 int moe_combine_pairs(const float *y_rows, const int32_t *pair_rows, int64_t T, int k, int64_t H, uint16_t *out,
                       void *stream);
 
+/*
+ * Training the layer's routing and moving its tokens, with the gradients, and the products
+ * of a few rows with 4-bit weights.  The sources describe inference; these calls are the
+ * transposes of moe_gather_pairs, moe_combine_pairs and moe_route, in the types that a
+ * training step uses, and the layer's projections one at a time.
+ *
+ * A training step over a user's own expert products:
+ *   moe_route, moe_permute (pair_rows given), moe_dispatch_rows, products,
+ *   moe_combine_rows; then moe_combine_rows_backward (gradients of the expert rows and of
+ *   the routing weights), the products' gradients, moe_dispatch_rows_backward and
+ *   moe_route_backward.
+ * A decode step of a few tokens without a sort or a copy, rows in pair order:
+ *   moe_route, mxfp4_matvec (gate_up, MOE_FLAG_SWIGLU, rows_per_x = k, row_ids = ids),
+ *   mxfp4_matvec (down, fp32 out, row_ids = ids), moe_combine_rows (pair_rows NULL).
+ */
+
+/* Element types of the calls below. */
+typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 } moe_dtype;
+
+/*
+ * moe_dispatch_rows -- token rows to expert rows.  For pair p = t*k + j with row
+ * r = pair_rows[p] and weight s = weights[p] (1 when weights is NULL):
+ *   rows[r] = s * x[t]
+ * moe_dispatch_rows_backward -- its gradient, given drows:
+ *   dx[t]       = sum over j of s * drows[r]       (slot order)
+ *   dweights[p] = sum over h of x[t, h] * drows[r, h]   (x and dweights both given or NULL)
+ * moe_combine_rows -- expert rows back to token rows:
+ *   out[t] = sum over j of s * rows[r]             (slot order)
+ * moe_combine_rows_backward -- its gradient, given dout:
+ *   drows[r]    = s * dout[t]
+ *   dweights[p] = sum over h of dout[t, h] * rows[r, h] (rows and dweights both given or NULL)
+ *
+ *   x, dx, out, dout  [T, H] of x_dtype / out_dtype;  rows, drows  [R, H] of rows_dtype
+ *   *_stride          elements from one row to the next (a row's elements are contiguous);
+ *                     inputs may repeat rows (stride 0), an output's stride is >= H
+ *   pair_rows         int32 [T*k] (moe_permute's inverse) or NULL: pair p has row p (R >= T*k)
+ *   weights, dweights fp32 [T*k]
+ * A pair with pair_rows[p] < 0 is dropped: neither its row nor its weight is read, it adds
+ * nothing, its dweights is 0; a token whose pairs are all dropped gets zeros.  An entry
+ * >= R is treated so too and raises MOE_DEVERR_OUT_OF_BOUNDS.  Rows that no pair names
+ * are left as they were.  The calls that write rows (moe_dispatch_rows,
+ * moe_combine_rows_backward) need the entries that are not dropped to be distinct, as
+ * moe_permute's are; the others may name a row twice.  Products and sums are fp32 in a
+ * fixed order, every result is rounded once; outputs must not alias inputs.
+ * Types: rows_dtype equal to the token side's type, or MOE_DTYPE_F32 (else
+ * MOE_ERR_UNSUPPORTED).  Sizes: T, H, R >= 1; 1 <= k <= 8; T*k, R, H < 2^31; pointers
+ * aligned to their elements (16-byte aligned rows and strides and H % 8 == 0 are the
+ * fast case).  Errors: MOE_ERR_INVALID_ARG for null pointers, sizes, strides, alignment.
+ */
+int moe_dispatch_rows(const void *x, int x_dtype, int64_t x_stride, int64_t T, int64_t H, int k,
+                      const int32_t *pair_rows, const float *weights, int64_t R, void *rows,
+                      int rows_dtype, int64_t rows_stride, void *stream);
+int moe_dispatch_rows_backward(const void *drows, int rows_dtype, int64_t rows_stride, int64_t T,
+                               int64_t H, int k, int64_t R, const int32_t *pair_rows,
+                               const float *weights, const void *x, int64_t x_stride, void *dx,
+                               int x_dtype, int64_t dx_stride, float *dweights, void *stream);
+int moe_combine_rows(const void *rows, int rows_dtype, int64_t rows_stride, int64_t T, int64_t H, int k,
+                     int64_t R, const int32_t *pair_rows, const float *weights, void *out,
+                     int out_dtype, int64_t out_stride, void *stream);
+int moe_combine_rows_backward(const void *dout, int out_dtype, int64_t dout_stride, int64_t T, int64_t H,
+                              int k, const int32_t *pair_rows, const float *weights, const void *rows,
+                              int64_t rows_stride, int64_t R, void *drows, int rows_dtype,
+                              int64_t drows_stride, float *dweights, void *stream);
+
+/*
+ * moe_route_backward -- gradient of moe_route's weights with respect to the router logits:
+ *   dlogits[t, ids[t, j]] = w_j * (dw_j - sum over i of w_i * dw_i), every other entry 0
+ *   dweights fp32 [T, k]; ids int32 [T, k] and weights fp32 [T, k] as moe_route wrote them;
+ *   dlogits fp32 [T, E], written whole
+ * Slots with id -1 (moe_route's empty slots) are skipped whatever their weights hold; any
+ * other id outside [0, E) is skipped and raises MOE_DEVERR_BAD_EXPERT_ID; two slots of one
+ * expert add.  Sizes: T >= 1; 1 <= E <= 256 (else MOE_ERR_UNSUPPORTED); 1 <= k <=
+ * min(E, 8); T*k < 2^31.  Errors: MOE_ERR_INVALID_ARG for null pointers or sizes.
+ */
+int moe_route_backward(const float *dweights, const int32_t *ids, const float *weights, int64_t T,
+                       int64_t E, int k, float *dlogits, void *stream);
+
+/*
+ * mxfp4_matvec / nvfp4_matvec -- products of a few rows with 4-bit weights:
+ *   y[r, n] = s2 * sum over kk of W[e, n, kk] * x[r / rows_per_x, kk] + bias[e, n]
+ *   out[r]  = y[r]                                        [R, N]     (flags 0)
+ *   out[r, i] = clamped SwiGLU of gate y[r, 2i], up y[r, 2i+1]  [R, N/2] (MOE_FLAG_SWIGLU)
+ * with e = row_ids[r], or 0 when row_ids is NULL (then E must be 1).
+ *   x        [ceil(R / rows_per_x), K] of x_dtype (bf16 or fp16), rows x_stride elements
+ *            apart; rows_per_x consecutive rows r share a row of x (k for the pairs of
+ *            a token, 1 otherwise)
+ *   blocks   uint8 [E, N, K/2]; scales uint8 [E, N, K/32] E8M0 (mxfp4) or [E, N, K/16]
+ *            E4M3 (nvfp4), as for mxfp4_dequantize / nvfp4_dequantize
+ *   scale2   fp32 (nvfp4) [E], with MOE_FLAG_SWIGLU [E, 2] (gate, up), or NULL (= 1)
+ *   bias     fp32 [E, N] or NULL;  alpha, limit: used with MOE_FLAG_SWIGLU only
+ *   out      of out_dtype: x_dtype or MOE_DTYPE_F32
+ * Sums in fp32, one rounding.  A row whose id falls outside [0, E) is left unwritten and
+ * raises MOE_DEVERR_BAD_EXPERT_ID; an invalid scale byte that is read makes its outputs
+ * NaN and raises MOE_DEVERR_BAD_SCALE.  Meant for decode, where each weight byte serves
+ * few rows and HBM bounds the product.  Sizes: 1 <= R <= MOE_MATVEC_MAX_ROWS; 1 <= E <=
+ * 256; N, K <= 2^24 (beyond: MOE_ERR_UNSUPPORTED); K % 32 == 0; N even with
+ * MOE_FLAG_SWIGLU.  x, blocks and scales 16-byte aligned, x_stride a multiple of 8.
+ * Errors: MOE_ERR_INVALID_ARG for null pointers, sizes, alignment, flags;
+ * MOE_ERR_UNSUPPORTED for types.
+ */
+#define MOE_FLAG_SWIGLU 0x2u
+#define MOE_MATVEC_MAX_ROWS 1024
+int mxfp4_matvec(const void *x, int x_dtype, int64_t x_stride, int rows_per_x, int64_t R, int64_t N,
+                 int64_t K, int64_t E, const int32_t *row_ids, const uint8_t *blocks,
+                 const uint8_t *scales, const float *bias, uint32_t flags, float alpha, float limit,
+                 void *out, int out_dtype, void *stream);
+int nvfp4_matvec(const void *x, int x_dtype, int64_t x_stride, int rows_per_x, int64_t R, int64_t N,
+                 int64_t K, int64_t E, const int32_t *row_ids, const uint8_t *blocks,
+                 const uint8_t *scales, const float *scale2, const float *bias, uint32_t flags,
+                 float alpha, float limit, void *out, int out_dtype, void *stream);
+
 /* Static English text for a moe_status value. */
 const char *moe_status_string(int status);
 
@@ -399,12 +513,15 @@ int moe_mxfp4_forward_noalloc(const uint16_t *x, int64_t T, int64_t H, int64_t I
  */
 #define MOE_PROFILE_STAGES 7
 enum {
-    MOE_STAGE_ROUTE = 0,   /* moe_route                                   */
+    MOE_STAGE_ROUTE = 0,   /* moe_route, moe_route_backward               */
     MOE_STAGE_PERMUTE = 1, /* pair histogram / scan / stable scatter      */
-    MOE_STAGE_GATHER = 2,  /* expert-ordered copy of the inputs           */
-    MOE_STAGE_GATE_UP = 3, /* gate_up grouped GEMM + bias + clamped SwiGLU */
-    MOE_STAGE_DOWN = 4,    /* down grouped GEMM + bias + routing weight   */
-    MOE_STAGE_COMBINE = 5, /* per-token sum of the k expert rows          */
+    MOE_STAGE_GATHER = 2,  /* expert-ordered copy of the inputs; moe_dispatch_rows,
+                              moe_combine_rows_backward                   */
+    MOE_STAGE_GATE_UP = 3, /* gate_up grouped GEMM + bias + clamped SwiGLU; the matvecs
+                              with MOE_FLAG_SWIGLU                        */
+    MOE_STAGE_DOWN = 4,    /* down grouped GEMM + bias + routing weight; the other matvecs */
+    MOE_STAGE_COMBINE = 5, /* per-token sum of the k expert rows; moe_combine_rows,
+                              moe_dispatch_rows_backward                  */
     MOE_STAGE_DEQUANT = 6  /* mxfp4_ / nvfp4_dequantize (+ _from_host)   */
 };
 int moe_profile_enable(int on);

@@ -24,12 +24,16 @@ __all__ = [
     "nvfp4_dequantize", "moe_nvfp4_forward_ex", "moe_router_route",
     "mxfp4_dequantize_from_host", "nvfp4_dequantize_from_host", "moe_permute", "moe_token_tile_rows",
     "MOE_DEVERR_BAD_LOGIT", "MOE_DEVERR_OUT_OF_BOUNDS", "use_checked_library", "moe_gather_pairs", "moe_mxfp4_expert_rows",
-    "moe_combine_pairs",
+    "moe_combine_pairs", "moe_dispatch_rows", "moe_dispatch_rows_backward", "moe_combine_rows",
+    "moe_combine_rows_backward", "moe_route_backward", "mxfp4_matvec", "nvfp4_matvec", "MOE_FLAG_SWIGLU",
+    "MOE_MATVEC_MAX_ROWS",
 ]
 
 MOE_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
 MOE_FLAG_WEIGHT_ON_INPUT = 0x1
+MOE_FLAG_SWIGLU = 0x2
+MOE_MATVEC_MAX_ROWS = 1024
 MOE_DEVERR_BAD_EXPERT_ID = 0x1
 MOE_DEVERR_BAD_SCALE = 0x2
 MOE_DEVERR_TIMEOUT = 0x4
@@ -43,6 +47,8 @@ EXPORTED_SYMBOLS = (
     "nvfp4_dequantize", "moe_nvfp4_forward_ex", "moe_router_route",
     "mxfp4_dequantize_from_host", "nvfp4_dequantize_from_host", "moe_permute", "moe_token_tile_rows",
     "moe_gather_pairs", "moe_mxfp4_expert_rows", "moe_combine_pairs",
+    "moe_dispatch_rows", "moe_dispatch_rows_backward", "moe_combine_rows", "moe_combine_rows_backward",
+    "moe_route_backward", "mxfp4_matvec", "nvfp4_matvec",
 )
 PROFILE_STAGES = ("route", "permute", "gather", "gate_up", "down", "combine", "dequant")
 
@@ -132,6 +138,21 @@ def load_library():
     lib.moe_mxfp4_expert_rows.restype = i32
     lib.moe_combine_pairs.argtypes = [p, p, i64, i32, i64, p, p]
     lib.moe_combine_pairs.restype = i32
+    lib.moe_dispatch_rows.argtypes = [p, i32, i64, i64, i64, i32, p, p, i64, p, i32, i64, p]
+    lib.moe_dispatch_rows.restype = i32
+    lib.moe_dispatch_rows_backward.argtypes = [p, i32, i64, i64, i64, i32, i64, p, p, p, i64, p, i32, i64, p, p]
+    lib.moe_dispatch_rows_backward.restype = i32
+    lib.moe_combine_rows.argtypes = [p, i32, i64, i64, i64, i32, i64, p, p, p, i32, i64, p]
+    lib.moe_combine_rows.restype = i32
+    lib.moe_combine_rows_backward.argtypes = [p, i32, i64, i64, i64, i32, p, p, p, i64, i64, p, i32, i64, p, p]
+    lib.moe_combine_rows_backward.restype = i32
+    lib.moe_route_backward.argtypes = [p, p, p, i64, i64, i32, p, p]
+    lib.moe_route_backward.restype = i32
+    matvec = [p, i32, i64, i32, i64, i64, i64, i64, p, p, p]
+    lib.mxfp4_matvec.argtypes = matvec + [p, ctypes.c_uint32, f32, f32, p, i32, p]
+    lib.mxfp4_matvec.restype = i32
+    lib.nvfp4_matvec.argtypes = matvec + [p, p, ctypes.c_uint32, f32, f32, p, i32, p]
+    lib.nvfp4_matvec.restype = i32
     lib.moe_profile_read.argtypes = [p, p]
     lib.moe_profile_read.restype = i32
     _libs[path] = lib
@@ -426,6 +447,213 @@ def moe_combine_pairs(y_rows, pair_rows, T: int, k: int, out=None, stream=None):
                                           _dev(out, torch.bfloat16, "out"), _stream(stream))
     _check("moe_combine_pairs", rc)
     return out
+
+
+# ---- training and few-token calls: bf16, fp16 and fp32, strided rows -----------------
+_DTYPE_CODES = {}
+
+
+def _dtype_code(dtype, name):
+    import torch
+    if not _DTYPE_CODES:
+        _DTYPE_CODES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
+        raise ValueError(f"{name}: expected bfloat16, float16 or float32, got {dtype}")
+    return code
+
+
+class _Call:
+    """Argument marshalling of one call: every tensor on the current CUDA device, outputs
+    allocated for the stream the call runs on, and tensors used on a stream other than
+    the current one kept from the allocator until that stream has run the call."""
+
+    def __init__(self, like, stream):
+        import torch
+        self.torch = torch
+        self.device = like.device
+        if not like.is_cuda or like.device.index != torch.cuda.current_device():
+            raise ValueError(f"expected tensors on the current CUDA device, got one on {like.device}")
+        current = torch.cuda.current_stream()
+        self.side = stream if stream is not None and stream != current else None
+        self.stream = ctypes.c_void_p((stream or current).cuda_stream)
+
+    def empty(self, shape, dtype):
+        if self.side is None:
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+        with self.torch.cuda.stream(self.side):
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _use(self, t, name):
+        if t.device != self.device:
+            raise ValueError(f"{name}: on {t.device}, expected {self.device}")
+        if self.side is not None:
+            t.record_stream(self.side)
+
+    def flat(self, t, dtype, name, numel):
+        """Contiguous tensor of `numel` elements (None stays None)."""
+        if t is None:
+            return None
+        if t.dtype != dtype or t.numel() != numel or not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous {dtype} tensor of {numel} elements, got "
+                             f"{t.dtype} {tuple(t.shape)} (contiguous={t.is_contiguous()})")
+        self._use(t, name)
+        return t.data_ptr()
+
+    def rows(self, t, name, shape, dtype=None):
+        """2-D tensor of contiguous rows, any row stride: (pointer, dtype code, stride)."""
+        if t is None:
+            return None, 0, 0
+        code = _dtype_code(t.dtype, name)
+        if tuple(t.shape) != shape or (dtype is not None and t.dtype != dtype) or (shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name}: expected {shape}{'' if dtype is None else f' of {dtype}'} with contiguous rows, "
+                             f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+        self._use(t, name)
+        return t.data_ptr(), code, t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def moe_dispatch_rows(x, pair_rows, k: int, weights=None, n_rows: Optional[int] = None, dtype=None, rows=None,
+                      stream=None):
+    """Token rows to expert rows: rows[pair_rows[t*k + j]] = weights[t, j] * x[t].
+    x [T, H] bf16, fp16 or fp32 with any row stride; pair_rows int32 [T*k] (moe_permute's,
+    -1 for a dropped pair) or None (row p for pair p); weights fp32 [T, k] or None (1).
+    Writes and returns rows [n_rows, H] (T*k rows of x's type unless rows, n_rows or dtype
+    say otherwise); rows that no pair names are left as they were."""
+    c = _Call(x, stream)
+    T, H = x.shape
+    if rows is None:
+        rows = c.empty((T * k if n_rows is None else n_rows, H), dtype or x.dtype)
+    xp, xd, xs = c.rows(x, "x", (T, H))
+    rp, rd, rs = c.rows(rows, "rows", (rows.shape[0], H), dtype)
+    _check("moe_dispatch_rows", load_library().moe_dispatch_rows(
+        xp, xd, xs, T, H, int(k), c.flat(pair_rows, c.torch.int32, "pair_rows", T * k),
+        c.flat(weights, c.torch.float32, "weights", T * k), rows.shape[0], rp, rd, rs, c.stream))
+    return rows
+
+
+def moe_dispatch_rows_backward(drows, pair_rows, T: int, k: int, weights=None, x=None, dtype=None, dx=None,
+                               dweights=None, stream=None):
+    """Gradient of moe_dispatch_rows: dx[t] = sum_j weights[t, j] * drows[pair_rows[t*k + j]]
+    and, when x is given, dweights[t, j] = <x[t], drows[pair_rows[t*k + j]]> (fp32 [T, k]).
+    Returns dx, or (dx, dweights)."""
+    c = _Call(drows, stream)
+    R, H = drows.shape
+    if dx is None:
+        dx = c.empty((T, H), dtype or (drows.dtype if x is None else x.dtype))
+    if x is not None and dweights is None:
+        dweights = c.empty((T, k), c.torch.float32)
+    rp, rd, rs = c.rows(drows, "drows", (R, H))
+    dp, dd, ds = c.rows(dx, "dx", (T, H), dtype)
+    xp, _, xs = c.rows(x, "x", (T, H), dx.dtype)
+    _check("moe_dispatch_rows_backward", load_library().moe_dispatch_rows_backward(
+        rp, rd, rs, T, H, int(k), R, c.flat(pair_rows, c.torch.int32, "pair_rows", T * k),
+        c.flat(weights, c.torch.float32, "weights", T * k), xp, xs, dp, dd, ds,
+        c.flat(dweights, c.torch.float32, "dweights", T * k), c.stream))
+    return dx if x is None else (dx, dweights)
+
+
+def moe_combine_rows(rows, pair_rows, T: int, k: int, weights=None, dtype=None, out=None, stream=None):
+    """Expert rows back to token rows: out[t] = sum_j weights[t, j] * rows[pair_rows[t*k + j]]
+    in slot order, fp32, rounded once.  rows [R, H] bf16, fp16 or fp32 with any row stride;
+    pair_rows and weights as for moe_dispatch_rows.  out [T, H] of `dtype` (rows' type by
+    default; fp32 rows may go to bf16 or fp16)."""
+    c = _Call(rows, stream)
+    R, H = rows.shape
+    if out is None:
+        out = c.empty((T, H), dtype or rows.dtype)
+    rp, rd, rs = c.rows(rows, "rows", (R, H))
+    op, od, os_ = c.rows(out, "out", (T, H), dtype)
+    _check("moe_combine_rows", load_library().moe_combine_rows(
+        rp, rd, rs, T, H, int(k), R, c.flat(pair_rows, c.torch.int32, "pair_rows", T * k),
+        c.flat(weights, c.torch.float32, "weights", T * k), op, od, os_, c.stream))
+    return out
+
+
+def moe_combine_rows_backward(dout, pair_rows, k: int, weights=None, y_rows=None, n_rows: Optional[int] = None,
+                              dtype=None, drows=None, dweights=None, stream=None):
+    """Gradient of moe_combine_rows: drows[pair_rows[t*k + j]] = weights[t, j] * dout[t] and,
+    when the forward pass's y_rows [R, H] is given, dweights[t, j] = <dout[t],
+    y_rows[pair_rows[t*k + j]]> (fp32 [T, k]).  drows is [R, H] of y_rows' type (n_rows, or
+    T*k, rows of dout's type without y_rows); rows that no pair names are left as they
+    were.  Returns drows, or (drows, dweights)."""
+    c = _Call(dout, stream)
+    T, H = dout.shape
+    if drows is None:
+        n = y_rows.shape[0] if y_rows is not None else T * k if n_rows is None else n_rows
+        drows = c.empty((n, H), dtype or (dout.dtype if y_rows is None else y_rows.dtype))
+    R = drows.shape[0]
+    if y_rows is not None and dweights is None:
+        dweights = c.empty((T, k), c.torch.float32)
+    op, od, os_ = c.rows(dout, "dout", (T, H))
+    dp, dd, ds = c.rows(drows, "drows", (R, H), dtype)
+    yp, _, ys = c.rows(y_rows, "y_rows", (R, H), drows.dtype)
+    _check("moe_combine_rows_backward", load_library().moe_combine_rows_backward(
+        op, od, os_, T, H, int(k), c.flat(pair_rows, c.torch.int32, "pair_rows", T * k),
+        c.flat(weights, c.torch.float32, "weights", T * k), yp, ys, R, dp, dd, ds,
+        c.flat(dweights, c.torch.float32, "dweights", T * k), c.stream))
+    return drows if y_rows is None else (drows, dweights)
+
+
+def moe_route_backward(dweights, ids, weights, E: int, dlogits=None, stream=None):
+    """Gradient of moe_route's weights: fp32 dweights [T, k], the ids and weights moe_route
+    returned -> fp32 dlogits [T, E], zero for the experts that were not chosen."""
+    c = _Call(dweights, stream)
+    T, k = dweights.shape
+    if dlogits is None:
+        dlogits = c.empty((T, E), c.torch.float32)
+    _check("moe_route_backward", load_library().moe_route_backward(
+        c.flat(dweights, c.torch.float32, "dweights", T * k), c.flat(ids, c.torch.int32, "ids", T * k),
+        c.flat(weights, c.torch.float32, "weights", T * k), T, int(E), k,
+        c.flat(dlogits, c.torch.float32, "dlogits", T * E), c.stream))
+    return dlogits
+
+
+def _matvec(name, block, x, blocks, scales, scale2, bias, row_ids, rows_per_x, swiglu, alpha, limit, out_dtype, out,
+            stream):
+    c = _Call(x, stream)
+    torch = c.torch
+    Tx, K = x.shape
+    E, N, Kh = blocks.shape if blocks.dim() == 3 else (1, *blocks.shape)
+    if Kh * 2 != K:
+        raise ValueError(f"{name}: x has {K} columns, the weights {2 * Kh}")
+    R = Tx * rows_per_x if row_ids is None else row_ids.numel()
+    if -(-R // rows_per_x) != Tx:
+        raise ValueError(f"{name}: {R} rows at {rows_per_x} per row of x do not make the {Tx} rows of x")
+    shape = (R, N // 2 if swiglu else N)
+    if out is None:
+        out = c.empty(shape, out_dtype or x.dtype)
+    if not out.is_contiguous():
+        raise ValueError("out: expected a contiguous tensor")
+    xp, xd, xs = c.rows(x, "x", (Tx, K))
+    op, od, _ = c.rows(out, "out", shape, out_dtype)
+    args = [xp, xd, xs, int(rows_per_x), R, N, K, E, c.flat(row_ids, torch.int32, "row_ids", R),
+            c.flat(blocks, torch.uint8, "blocks", E * N * Kh),
+            c.flat(scales, torch.uint8, "scales", E * N * (K // block))]
+    if block == 16:
+        args.append(c.flat(scale2, torch.float32, "scale2", 2 * E if swiglu else E))
+    args += [c.flat(bias, torch.float32, "bias", E * N), MOE_FLAG_SWIGLU if swiglu else 0, float(alpha), float(limit),
+             op, od, c.stream]
+    _check(name, getattr(load_library(), name)(*args))
+    return out
+
+
+def mxfp4_matvec(x, blocks, scales, bias=None, row_ids=None, rows_per_x: int = 1, swiglu: bool = False,
+                 alpha: float = 1.702, limit: float = 7.0, out_dtype=None, out=None, stream=None):
+    """Products of a few rows with MXFP4 weights: out[r] = W[row_ids[r]] x[r // rows_per_x] +
+    bias[row_ids[r]], followed with `swiglu` by the clamped SwiGLU of the interleaved gate
+    and up outputs.  x [*, K] bf16 or fp16; blocks uint8 [E, N, K/2] (or [N, K/2] for one
+    matrix), scales [E, N, K/32]; bias fp32 [E, N] or None; row_ids int32 [R] or None (one
+    matrix).  out [R, N] or [R, N/2] of x's type or fp32."""
+    return _matvec("mxfp4_matvec", 32, x, blocks, scales, None, bias, row_ids, rows_per_x, swiglu, alpha, limit,
+                   out_dtype, out, stream)
+
+
+def nvfp4_matvec(x, blocks, scales, scale2=None, bias=None, row_ids=None, rows_per_x: int = 1, swiglu: bool = False,
+                 alpha: float = 1.702, limit: float = 7.0, out_dtype=None, out=None, stream=None):
+    """mxfp4_matvec over NVFP4 weights: E4M3 scales [E, N, K/16] and fp32 scale2 [E] ([E, 2],
+    gate and up, with `swiglu`) or None; scale2 multiplies the product before the bias."""
+    return _matvec("nvfp4_matvec", 16, x, blocks, scales, scale2, bias, row_ids, rows_per_x, swiglu, alpha, limit,
+                   out_dtype, out, stream)
 
 
 def moe_token_tile_rows(T: int, H: int, I: int, E: int, k: int, nvfp4: bool = False) -> int:

@@ -8,9 +8,11 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <tuple>
+#include <type_traits>
 #include <utility>
 #include <vector>
 
@@ -26,6 +28,8 @@
 #include "dequant.cuh"
 #include "gemm_mxf.cuh"
 #include "gemm_swap.cuh"
+#include "matvec.cuh"
+#include "pair_rows.cuh"
 #include "permute.cuh"
 #include "split.cuh"
 #include "route.cuh"
@@ -669,6 +673,178 @@ int device_view_of_host(const void *host, int64_t bytes, const void **dev) {
     return MOE_OK;
 }
 
+// ---- token rows <-> expert rows ------------------------------------------------
+size_t dtype_size(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : (dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_F16) ? 2 : 0; }
+
+// One side of a spread or sum: its rows, their stride in elements and element size.
+struct RowsArg {
+    const void *p;
+    int64_t stride;
+    size_t size;
+};
+
+// Elements per chunk: 8 (16-byte words) when every row of every operand starts on a
+// 16-byte boundary and H is a multiple of 8; else 2 under the same rule for two
+// elements; else 1.
+int chunk_elems(int64_t H, std::initializer_list<RowsArg> rows) {
+    for (const int ve : {8, 2}) {
+        bool ok = H % ve == 0;
+        for (const RowsArg &a : rows) {
+            const size_t word = std::min<size_t>(16, ve * a.size);
+            ok = ok && (!a.p || (aligned(a.p, word) && (a.stride * (int64_t)a.size) % (int64_t)word == 0));
+        }
+        if (ok) return ve;
+    }
+    return 1;
+}
+
+// Threads per token: 32 (a warp) once the tokens alone give every SM 32 warps, up to a
+// whole block of 256 below that, and no more than the row has chunks for.
+int pair_group(int64_t T, int64_t chunks) {
+    int g = 32;
+    while (g < moe::kPairThreads && T * g < (int64_t)sm_count() * 1024 && g < chunks) g *= 2;
+    return g;
+}
+
+bool pair_sizes_ok(int64_t T, int64_t H, int k, int64_t R) {
+    return T >= 1 && H >= 1 && k >= 1 && k <= 8 && R >= 1 && T * k < (int64_t(1) << 31) && R < (int64_t(1) << 31) &&
+           H < (int64_t(1) << 31);
+}
+
+template <class Tok, class Row, int VE, int KM, bool kDot>
+int launch_spread(moe::PairRows q, const void *a, int64_t a_stride, const void *src, int64_t src_stride, void *rows,
+                  int64_t rows_stride, cudaStream_t s) {
+    q.group = pair_group(q.T, q.H / VE);
+    const int64_t grid = moe::ceil_div(q.T, moe::kPairThreads / q.group);
+    StageScope scope(MOE_STAGE_GATHER, s);
+    launch_pdl(moe::spread_rows_kernel<Tok, Row, VE, KM, kDot>, dim3((unsigned)grid), dim3(moe::kPairThreads), 0, s, q,
+               static_cast<const Tok *>(a), a_stride, static_cast<const Row *>(src), src_stride,
+               static_cast<Row *>(rows), rows_stride);
+    return launch_check();
+}
+
+template <class Tok, class Row, int VE, int KM, bool kDot>
+int launch_sum(moe::PairRows q, const void *rows, int64_t rows_stride, const void *a, int64_t a_stride, void *out,
+               int64_t out_stride, cudaStream_t s) {
+    q.group = pair_group(q.T, q.H / VE);
+    const int64_t grid = moe::ceil_div(q.T, moe::kPairThreads / q.group);
+    StageScope scope(MOE_STAGE_COMBINE, s);
+    launch_pdl(moe::sum_rows_kernel<Tok, Row, VE, KM, kDot>, dim3((unsigned)grid), dim3(moe::kPairThreads), 0, s, q,
+               static_cast<const Row *>(rows), rows_stride, static_cast<const Tok *>(a), a_stride,
+               static_cast<Tok *>(out), out_stride);
+    return launch_check();
+}
+
+// Calls f(Tok{}, Row{}, VE, KM) of the compiled combinations: the token side and the
+// expert side of one type, or fp32 expert rows.
+template <int N>
+using Int = std::integral_constant<int, N>;
+template <class Tok, class Row, class F>
+int with_shape(int ve, int k, F &&f) {
+    if (k <= 4) {
+        if (ve == 8) return f(Tok{}, Row{}, Int<8>{}, Int<4>{});
+        if (ve == 2) return f(Tok{}, Row{}, Int<2>{}, Int<4>{});
+        return f(Tok{}, Row{}, Int<1>{}, Int<4>{});
+    }
+    if (ve == 8) return f(Tok{}, Row{}, Int<8>{}, Int<8>{});
+    if (ve == 2) return f(Tok{}, Row{}, Int<2>{}, Int<8>{});
+    return f(Tok{}, Row{}, Int<1>{}, Int<8>{});
+}
+template <class F>
+int with_types(int tok, int row, int ve, int k, F &&f) {
+    if (tok == MOE_DTYPE_BF16 && row == MOE_DTYPE_BF16) return with_shape<__nv_bfloat16, __nv_bfloat16>(ve, k, f);
+    if (tok == MOE_DTYPE_F16 && row == MOE_DTYPE_F16) return with_shape<__half, __half>(ve, k, f);
+    if (tok == MOE_DTYPE_F32 && row == MOE_DTYPE_F32) return with_shape<float, float>(ve, k, f);
+    if (tok == MOE_DTYPE_BF16 && row == MOE_DTYPE_F32) return with_shape<__nv_bfloat16, float>(ve, k, f);
+    if (tok == MOE_DTYPE_F16 && row == MOE_DTYPE_F32) return with_shape<__half, float>(ve, k, f);
+    return MOE_ERR_UNSUPPORTED;
+}
+
+// rows[r(p)] = s_p a[t]; with src: dots[p] = <a[t], src[r(p)]>.
+int spread(const void *a, int a_dtype, int64_t a_stride, int64_t T, int64_t H, int k, const int32_t *pair_rows,
+           const float *weights, const void *src, int64_t src_stride, int64_t R, void *rows, int rows_dtype,
+           int64_t rows_stride, float *dots, cudaStream_t s) {
+    if (!a || !rows || (src == nullptr) != (dots == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!pair_sizes_ok(T, H, k, R) || !dtype_size(a_dtype) || !dtype_size(rows_dtype)) return MOE_ERR_INVALID_ARG;
+    if (!pair_rows && R < T * k) return MOE_ERR_INVALID_ARG;
+    if (a_stride < 0 || (src && src_stride < 0) || rows_stride < H) return MOE_ERR_INVALID_ARG;
+    if (!aligned(a, dtype_size(a_dtype)) || !aligned(src, dtype_size(rows_dtype)) ||
+        !aligned(rows, dtype_size(rows_dtype)) || !aligned(pair_rows, 4) || !aligned(weights, 4) || !aligned(dots, 4))
+        return MOE_ERR_INVALID_ARG;
+    const moe::PairRows q{T, H, R, k, 0, pair_rows, weights, dots};
+    const int ve = chunk_elems(H, {{a, a_stride, dtype_size(a_dtype)},
+                                   {src, src_stride, dtype_size(rows_dtype)},
+                                   {rows, rows_stride, dtype_size(rows_dtype)}});
+    return with_types(a_dtype, rows_dtype, ve, k, [&](auto tok, auto row, auto v, auto km) {
+        using Tok = decltype(tok);
+        using Row = decltype(row);
+        return src ? launch_spread<Tok, Row, v.value, km.value, true>(q, a, a_stride, src, src_stride, rows, rows_stride, s)
+                   : launch_spread<Tok, Row, v.value, km.value, false>(q, a, a_stride, src, src_stride, rows, rows_stride, s);
+    });
+}
+
+// out[t] = sum_j s_p rows[r(p)]; with a: dots[p] = <a[t], rows[r(p)]>.
+int sum_rows(const void *rows, int rows_dtype, int64_t rows_stride, int64_t T, int64_t H, int k, int64_t R,
+             const int32_t *pair_rows, const float *weights, const void *a, int64_t a_stride, void *out, int out_dtype,
+             int64_t out_stride, float *dots, cudaStream_t s) {
+    if (!rows || !out || (a == nullptr) != (dots == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!pair_sizes_ok(T, H, k, R) || !dtype_size(out_dtype) || !dtype_size(rows_dtype)) return MOE_ERR_INVALID_ARG;
+    if (!pair_rows && R < T * k) return MOE_ERR_INVALID_ARG;
+    if (rows_stride < 0 || (a && a_stride < 0) || out_stride < H) return MOE_ERR_INVALID_ARG;
+    if (!aligned(rows, dtype_size(rows_dtype)) || !aligned(a, dtype_size(out_dtype)) ||
+        !aligned(out, dtype_size(out_dtype)) || !aligned(pair_rows, 4) || !aligned(weights, 4) || !aligned(dots, 4))
+        return MOE_ERR_INVALID_ARG;
+    const moe::PairRows q{T, H, R, k, 0, pair_rows, weights, dots};
+    const int ve = chunk_elems(H, {{rows, rows_stride, dtype_size(rows_dtype)},
+                                   {a, a_stride, dtype_size(out_dtype)},
+                                   {out, out_stride, dtype_size(out_dtype)}});
+    return with_types(out_dtype, rows_dtype, ve, k, [&](auto tok, auto row, auto v, auto km) {
+        using Tok = decltype(tok);
+        using Row = decltype(row);
+        return a ? launch_sum<Tok, Row, v.value, km.value, true>(q, rows, rows_stride, a, a_stride, out, out_stride, s)
+                 : launch_sum<Tok, Row, v.value, km.value, false>(q, rows, rows_stride, a, a_stride, out, out_stride, s);
+    });
+}
+
+// ---- products of a few rows with 4-bit weights ----------------------------------
+template <class X, class Out, bool kNv, bool kSwiGlu>
+int launch_matvec(const moe::MatvecParams &q, cudaStream_t s) {
+    const int n_out = kSwiGlu ? q.N / 2 : q.N;
+    StageScope scope(kSwiGlu ? MOE_STAGE_GATE_UP : MOE_STAGE_DOWN, s);
+    launch_pdl(moe::matvec_kernel<X, Out, kNv, kSwiGlu>, dim3((unsigned)moe::ceil_div(n_out, 8), (unsigned)q.R),
+               dim3(256), 0, s, q);
+    return launch_check();
+}
+
+template <bool kNv>
+int matvec(const void *x, int x_dtype, int64_t x_stride, int rows_per_x, int64_t R, int64_t N, int64_t K, int64_t E,
+           const int32_t *row_ids, const uint8_t *blocks, const uint8_t *scales, const float *scale2,
+           const float *bias, uint32_t flags, float alpha, float limit, void *out, int out_dtype, cudaStream_t s) {
+    if (!x || !blocks || !scales || !out) return MOE_ERR_INVALID_ARG;
+    if (flags & ~MOE_FLAG_SWIGLU) return MOE_ERR_INVALID_ARG;
+    const bool swiglu = (flags & MOE_FLAG_SWIGLU) != 0;
+    if (R < 1 || rows_per_x < 1 || N < 1 || K < 32 || K % 32 != 0 || E < 1 || (!row_ids && E != 1) || x_stride < 0 ||
+        (swiglu && N % 2 != 0))
+        return MOE_ERR_INVALID_ARG;
+    if (!dtype_size(x_dtype) || !dtype_size(out_dtype)) return MOE_ERR_INVALID_ARG;
+    if (R > MOE_MATVEC_MAX_ROWS || E > 256 || N > (1 << 24) || K > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+    if (x_dtype == MOE_DTYPE_F32 || (out_dtype != x_dtype && out_dtype != MOE_DTYPE_F32)) return MOE_ERR_UNSUPPORTED;
+    if (!aligned(x, 16) || (x_stride % 8) != 0 || !aligned(blocks, 16) || !aligned(scales, 16) || !aligned(row_ids, 4) ||
+        !aligned(scale2, 4) || !aligned(bias, 4) || !aligned(out, dtype_size(out_dtype)))
+        return MOE_ERR_INVALID_ARG;
+    const moe::MatvecParams q{x,       x_stride, rows_per_x, (int)R, (int)N, (int)K, (int)E, row_ids,
+                              blocks,  scales,   scale2,     bias,   alpha,  limit,  out};
+#define MOE_MATVEC(X, OUT) \
+    return swiglu ? launch_matvec<X, OUT, kNv, true>(q, s) : launch_matvec<X, OUT, kNv, false>(q, s)
+    if (x_dtype == MOE_DTYPE_BF16) {
+        if (out_dtype == MOE_DTYPE_F32) MOE_MATVEC(__nv_bfloat16, float);
+        MOE_MATVEC(__nv_bfloat16, __nv_bfloat16);
+    }
+    if (out_dtype == MOE_DTYPE_F32) MOE_MATVEC(__half, float);
+    MOE_MATVEC(__half, __half);
+#undef MOE_MATVEC
+}
+
 bool bank_sizes_ok(int64_t E, int64_t N, int64_t K, int64_t block) {
     return E >= 1 && N >= 1 && K >= block && K % block == 0 && E <= (int64_t(1) << 40) / N / K;
 }
@@ -840,6 +1016,73 @@ int moe_combine_pairs(const float *y_rows, const int32_t *pair_rows, int64_t T, 
     launch_pdl(moe::combine_pair_rows_kernel, dim3((unsigned)cgrid), dim3(256), 0, s, y_rows, pair_rows, T, k, H,
                out);
     return launch_check();
+}
+
+int moe_dispatch_rows(const void *x, int x_dtype, int64_t x_stride, int64_t T, int64_t H, int k,
+                      const int32_t *pair_rows, const float *weights, int64_t R, void *rows, int rows_dtype,
+                      int64_t rows_stride, void *stream) {
+    NvtxRange nvtx("moe_dispatch_rows");
+    return spread(x, x_dtype, x_stride, T, H, k, pair_rows, weights, nullptr, 0, R, rows, rows_dtype, rows_stride,
+                  nullptr, (cudaStream_t)stream);
+}
+
+int moe_dispatch_rows_backward(const void *drows, int rows_dtype, int64_t rows_stride, int64_t T, int64_t H, int k,
+                               int64_t R, const int32_t *pair_rows, const float *weights, const void *x,
+                               int64_t x_stride, void *dx, int x_dtype, int64_t dx_stride, float *dweights,
+                               void *stream) {
+    NvtxRange nvtx("moe_dispatch_rows_backward");
+    return sum_rows(drows, rows_dtype, rows_stride, T, H, k, R, pair_rows, weights, x, x_stride, dx, x_dtype, dx_stride,
+                    dweights, (cudaStream_t)stream);
+}
+
+int moe_combine_rows(const void *rows, int rows_dtype, int64_t rows_stride, int64_t T, int64_t H, int k, int64_t R,
+                     const int32_t *pair_rows, const float *weights, void *out, int out_dtype, int64_t out_stride,
+                     void *stream) {
+    NvtxRange nvtx("moe_combine_rows");
+    return sum_rows(rows, rows_dtype, rows_stride, T, H, k, R, pair_rows, weights, nullptr, 0, out, out_dtype,
+                    out_stride, nullptr, (cudaStream_t)stream);
+}
+
+int moe_combine_rows_backward(const void *dout, int out_dtype, int64_t dout_stride, int64_t T, int64_t H, int k,
+                              const int32_t *pair_rows, const float *weights, const void *rows, int64_t rows_stride,
+                              int64_t R, void *drows, int rows_dtype, int64_t drows_stride, float *dweights,
+                              void *stream) {
+    NvtxRange nvtx("moe_combine_rows_backward");
+    return spread(dout, out_dtype, dout_stride, T, H, k, pair_rows, weights, rows, rows_stride, R, drows, rows_dtype,
+                  drows_stride, dweights, (cudaStream_t)stream);
+}
+
+int moe_route_backward(const float *dweights, const int32_t *ids, const float *weights, int64_t T, int64_t E, int k,
+                       float *dlogits, void *stream) {
+    NvtxRange nvtx("moe_route_backward");
+    if (!dweights || !ids || !weights || !dlogits) return MOE_ERR_INVALID_ARG;
+    if (T < 1 || E < 1 || k < 1 || k > 8 || k > E || T * k >= (int64_t(1) << 31)) return MOE_ERR_INVALID_ARG;
+    if (E > 256) return MOE_ERR_UNSUPPORTED;
+    if (!aligned(dweights, 4) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(dlogits, 4))
+        return MOE_ERR_INVALID_ARG;
+    cudaStream_t s = (cudaStream_t)stream;
+    const bool wide = E % 4 == 0 && aligned(dlogits, 16);
+    const int64_t per = 256 / (wide ? E / 4 : E);
+    StageScope scope(MOE_STAGE_ROUTE, s);
+    launch_pdl(wide ? moe::route_backward_kernel<4> : moe::route_backward_kernel<1>,
+               dim3((unsigned)moe::ceil_div(T, per)), dim3(256), 0, s, dweights, ids, weights, T, (int)E, k, dlogits);
+    return launch_check();
+}
+
+int mxfp4_matvec(const void *x, int x_dtype, int64_t x_stride, int rows_per_x, int64_t R, int64_t N, int64_t K,
+                 int64_t E, const int32_t *row_ids, const uint8_t *blocks, const uint8_t *scales, const float *bias,
+                 uint32_t flags, float alpha, float limit, void *out, int out_dtype, void *stream) {
+    NvtxRange nvtx("mxfp4_matvec");
+    return matvec<false>(x, x_dtype, x_stride, rows_per_x, R, N, K, E, row_ids, blocks, scales, nullptr, bias, flags,
+                         alpha, limit, out, out_dtype, (cudaStream_t)stream);
+}
+
+int nvfp4_matvec(const void *x, int x_dtype, int64_t x_stride, int rows_per_x, int64_t R, int64_t N, int64_t K,
+                 int64_t E, const int32_t *row_ids, const uint8_t *blocks, const uint8_t *scales, const float *scale2,
+                 const float *bias, uint32_t flags, float alpha, float limit, void *out, int out_dtype, void *stream) {
+    NvtxRange nvtx("nvfp4_matvec");
+    return matvec<true>(x, x_dtype, x_stride, rows_per_x, R, N, K, E, row_ids, blocks, scales, scale2, bias, flags,
+                        alpha, limit, out, out_dtype, (cudaStream_t)stream);
 }
 
 int moe_permute(const int32_t *ids, int64_t T, int k, int64_t E, int tile_rows, int32_t *counts,

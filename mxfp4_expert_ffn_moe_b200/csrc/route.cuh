@@ -83,4 +83,54 @@ __global__ void __launch_bounds__(256) route_topk_kernel(const float *__restrict
     }
 }
 
+// Gradient of the routing weights with respect to the logits.  w = softmax over the k
+// chosen logits, so dlogits[t, ids[t, j]] = w_j (dw_j - sum_i w_i dw_i), and the logits
+// that were not chosen do not move the weights: 0.  Empty slots (id -1) give nothing; an
+// expert named by two slots of a token gets both, in slot order.  Bound by the stores of
+// the dense [T, E] gradient: one thread per VE experts of a token, so each store is a
+// whole word and nothing is cleared first; a token's k pairs are read by its threads
+// through L1.
+template <int VE>
+__global__ void __launch_bounds__(256) route_backward_kernel(const float *__restrict__ dweights,
+                                                             const int32_t *__restrict__ ids,
+                                                             const float *__restrict__ weights, int64_t T, int E,
+                                                             int k, float *__restrict__ dlogits) {
+    pdl_wait();
+    pdl_trigger();
+    const unsigned q = (unsigned)E / VE, per = 256u / q;
+    const unsigned tl = threadIdx.x / q, c = threadIdx.x - tl * q;
+    const int64_t t = (int64_t)blockIdx.x * per + tl;
+    if (tl >= per || t >= T) return;
+    float w[8], g[8];
+    int id[8];
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (j >= k) break;
+        id[j] = __ldg(ids + t * k + j);
+        const bool used = id[j] >= 0 && id[j] < E;
+        if (!used && id[j] != -1) raise_device_error(MOE_DEVERR_BAD_EXPERT_ID);
+        if (!used) id[j] = -1;
+        w[j] = used ? __ldg(weights + t * k + j) : 0.0f;
+        g[j] = used ? __ldg(dweights + t * k + j) : 0.0f;
+        s = fmaf(w[j], g[j], s);
+    }
+    float o[VE];
+#pragma unroll
+    for (int i = 0; i < VE; ++i) o[i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (j >= k) break;
+        const float v = w[j] * (g[j] - s);
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+            if (id[j] == (int)(c * VE) + i) o[i] += v;
+    }
+    float *dst = dlogits + t * E + c * VE;
+    if constexpr (VE == 4)
+        *reinterpret_cast<float4 *>(dst) = make_float4(o[0], o[1], o[2], o[3]);
+    else
+        dst[0] = o[0];
+}
+
 }  // namespace moe
