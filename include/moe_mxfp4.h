@@ -426,9 +426,11 @@ int moe_route_backward(const float *dweights, const int32_t *ids, const float *w
  *   out      of out_dtype: x_dtype or MOE_DTYPE_F32
  * Sums in fp32, one rounding.  A row whose id falls outside [0, E) is left unwritten and
  * raises MOE_DEVERR_BAD_EXPERT_ID; an invalid scale byte that is read makes its outputs
- * NaN and raises MOE_DEVERR_BAD_SCALE.  Meant for decode, where each weight byte serves
- * few rows and HBM bounds the product.  Sizes: 1 <= R <= MOE_MATVEC_MAX_ROWS; 1 <= E <=
- * 256; N, K <= 2^24 (beyond: MOE_ERR_UNSUPPORTED); K % 32 == 0; N even with
+ * NaN and raises MOE_DEVERR_BAD_SCALE.  bf16 values below 2^-31 of the largest finite one
+ * of their row of x count to within 2^-39 of that.  Meant for decode, where each weight
+ * byte serves few rows and HBM bounds the product: weights are read once for every 8
+ * rows of an expert.  Sizes: 1 <= R <= MOE_MATVEC_MAX_ROWS; 1 <= E <= 256; N <= 2^24;
+ * K <= 2^16 (beyond: MOE_ERR_UNSUPPORTED); K % 32 == 0; N even with
  * MOE_FLAG_SWIGLU.  x, blocks and scales 16-byte aligned, x_stride a multiple of 8.
  * Errors: MOE_ERR_INVALID_ARG for null pointers, sizes, alignment, flags;
  * MOE_ERR_UNSUPPORTED for types.

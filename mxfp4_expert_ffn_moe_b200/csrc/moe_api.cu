@@ -807,12 +807,46 @@ int sum_rows(const void *rows, int rows_dtype, int64_t rows_stride, int64_t T, i
 }
 
 // ---- products of a few rows with 4-bit weights ----------------------------------
+// Shared memory of a call.  Rows of x per tile: 8, or as many as fit beside two stages.
+// Stages: what keeps two CTAs on an SM, 2 at least and 4 at most.  0 stages: does not fit.
+moe::mv::Layout matvec_layout(int64_t R, int64_t K, int block, int limit) {
+    namespace mv = moe::mv;
+    mv::Layout L{};
+    L.chunks = (int)moe::ceil_div(K, mv::kStageK);
+    L.kc = (int)(moe::ceil_div(moe::ceil_div(K, L.chunks), 32) * 32);
+    L.chunks = (int)moe::ceil_div(K, L.kc);
+    L.ws = mv::weight_stride(L.kc);
+    L.ss = mv::scale_stride(L.kc, block);
+    L.xs = mv::x_row_stride((int)K);
+    const int stage = mv::kRows * (L.ws + L.ss), red = 2 * mv::kWarps * mv::kRows * mv::kTok * 4;
+    const int fixed = red + (int)sizeof(mv::Shared) + 1024;       // 1 KB is the system's
+    const int64_t fit = ((int64_t)limit - fixed - 2 * stage) / L.xs;
+    L.nt = (int)std::min<int64_t>(std::min<int64_t>(mv::kTok, R), fit);
+    if (L.nt < 1) return L;
+    const int x_bytes = (L.nt * L.xs + 127) / 128 * 128;
+    L.stages = (limit / 2 - fixed - x_bytes) / stage;
+    if (L.stages < 2) L.stages = (limit - fixed - x_bytes) / stage;
+    L.stages = std::max(2, std::min(L.stages, mv::kMaxStages));
+    L.ring = x_bytes;
+    L.red = L.ring + L.stages * stage;
+    L.total = L.red + red;
+    return L;
+}
+
 template <class X, class Out, bool kNv, bool kSwiGlu>
-int launch_matvec(const moe::MatvecParams &q, cudaStream_t s) {
-    const int n_out = kSwiGlu ? q.N / 2 : q.N;
+int launch_matvec(moe::mv::Params q, cudaStream_t s) {
+    namespace mv = moe::mv;
+    const int optin = max_smem_optin();
+    q.L = matvec_layout(q.R, q.K, kNv ? 16 : 32, optin);
+    if (q.L.stages < 2) return MOE_ERR_UNSUPPORTED;
+    auto kernel = mv::matvec_kernel<X, Out, kNv, kSwiGlu>;
+    if (!ensure_smem_attr(reinterpret_cast<const void *>(kernel), q.L.total)) return MOE_ERR_CUDA;
+    // at most every row alone, or every expert's last tile ragged
+    const int64_t slots = q.row_ids ? std::min<int64_t>(q.R, q.E + q.R / q.L.nt) : moe::ceil_div(q.R, q.L.nt);
+    const int per_sm = 2 * (q.L.total + (int)sizeof(mv::Shared) + 1024) <= optin + 1024 ? 2 : 1;
+    const int64_t grid = std::min<int64_t>(slots * moe::ceil_div(q.N, mv::kRows), (int64_t)sm_count() * per_sm);
     StageScope scope(kSwiGlu ? MOE_STAGE_GATE_UP : MOE_STAGE_DOWN, s);
-    launch_pdl(moe::matvec_kernel<X, Out, kNv, kSwiGlu>, dim3((unsigned)moe::ceil_div(n_out, 8), (unsigned)q.R),
-               dim3(256), 0, s, q);
+    launch_pdl(kernel, dim3((unsigned)grid), dim3(mv::kThreads), q.L.total, s, q);
     return launch_check();
 }
 
@@ -827,13 +861,13 @@ int matvec(const void *x, int x_dtype, int64_t x_stride, int rows_per_x, int64_t
         (swiglu && N % 2 != 0))
         return MOE_ERR_INVALID_ARG;
     if (!dtype_size(x_dtype) || !dtype_size(out_dtype)) return MOE_ERR_INVALID_ARG;
-    if (R > MOE_MATVEC_MAX_ROWS || E > 256 || N > (1 << 24) || K > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+    if (R > MOE_MATVEC_MAX_ROWS || E > moe::mv::kMaxExperts || N > (1 << 24) || K > (1 << 16)) return MOE_ERR_UNSUPPORTED;
     if (x_dtype == MOE_DTYPE_F32 || (out_dtype != x_dtype && out_dtype != MOE_DTYPE_F32)) return MOE_ERR_UNSUPPORTED;
     if (!aligned(x, 16) || (x_stride % 8) != 0 || !aligned(blocks, 16) || !aligned(scales, 16) || !aligned(row_ids, 4) ||
         !aligned(scale2, 4) || !aligned(bias, 4) || !aligned(out, dtype_size(out_dtype)))
         return MOE_ERR_INVALID_ARG;
-    const moe::MatvecParams q{x,       x_stride, rows_per_x, (int)R, (int)N, (int)K, (int)E, row_ids,
-                              blocks,  scales,   scale2,     bias,   alpha,  limit,  out};
+    const moe::mv::Params q{x,      x_stride, rows_per_x, (int)R, (int)N, (int)K, (int)E, row_ids,
+                            blocks, scales,   scale2,     bias,   alpha,  limit,  out,    {}};
 #define MOE_MATVEC(X, OUT) \
     return swiglu ? launch_matvec<X, OUT, kNv, true>(q, s) : launch_matvec<X, OUT, kNv, false>(q, s)
     if (x_dtype == MOE_DTYPE_BF16) {
