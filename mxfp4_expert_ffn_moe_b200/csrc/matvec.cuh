@@ -18,16 +18,19 @@
 //    the row's largest value and are rounded to 2^-39 of it below, far under the 2^-24 of
 //    the fp32 sum.  Products are then exact, the sums are fp32, the result is rounded once.
 //  * NVFP4 scales multiply the weights in f16 (exact).  E8M0 scales do not fit f16; they
-//    multiply the fp32 sums of their 32-element block, relative to the largest scale of the
-//    warp's slice of the row, so no intermediate overflows before the result does
-//    (blocks 2^-190 below the largest scale of the slice drop out).
-//  * Weights arrive by bulk asynchronous copies, one per row of a 16-row tile, into a ring
-//    of stages filled by a ninth warp; the scale bytes of each row, which start anywhere,
-//    come as the 16-byte granules that hold them.
-// An item is 16 weight rows x K against one tile of at most 8 rows of one expert; CTAs take
-// contiguous runs of items (expert by expert), so the rows of x are staged once per
-// expert a CTA meets.  The eight warps split K by 32-element blocks and their sums are
-// joined in warp order: the same call gives the same bits.
+//    multiply the fp32 sums of their 32-element block, relative to a scale of the warp's
+//    slice of the row, so that no intermediate overflows before the result does (blocks
+//    2^-126 below that scale drop out).  Each warp turns the scale bytes of its blocks into
+//    factors once per stage, a row to a lane, instead of in each of the lanes that use them.
+//  * Weights arrive as TMA boxes of 128 bytes x the item's rows, 128-byte swizzled (the 8
+//    rows x 4 words of a fragment load then fall into 32 different banks), into a ring of
+//    stages filled by a ninth warp.  An item's scale bytes are one contiguous run that
+//    starts anywhere: one bulk copy of the 16-byte granules that hold it.
+// An item is kRows weight rows x K against one tile of at most 8 rows of x of one expert;
+// CTAs take contiguous runs of items (expert by expert), so the rows of x are staged once
+// per expert a CTA meets.  kSplit warps share a group of rows, each with 4 blocks of 32
+// elements of every stage; their sums are joined in warp order, so the same call gives
+// the same bits.
 #pragma once
 #include <type_traits>
 
@@ -39,21 +42,38 @@
 namespace moe {
 namespace mv {
 
-constexpr int kRows = 16;              // weight rows of an item (mma M)
 constexpr int kTok = 8;                // rows of x of an item (mma N)
 constexpr int kWarps = 8;              // computing warps; one more issues the copies
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kMaxStages = 4;
-constexpr int kStageK = 4096;          // most elements of a weight row in one stage
 constexpr int kMaxExperts = 256;
+constexpr int kWarpBlocks = 4;         // 32-element blocks of a warp in one stage
 
-// Shared-memory layout of a call (host-computed; offsets and strides in bytes).
+// kSplit warps over the K of a group of 16 * kTiles weight rows.
+template <int kSplit_, int kTiles_>
+struct Tile {
+    static constexpr int kSplit = kSplit_, kTiles = kTiles_;
+    static constexpr int kGroups = kWarps / kSplit;
+    static constexpr int kGroupRows = 16 * kTiles;
+    static constexpr int kRows = kGroups * kGroupRows;           // weight rows of an item
+    static constexpr int kStageK = kSplit * kWarpBlocks * 32;    // their elements in a stage
+    static constexpr int kBoxBytes = kRows * 128;                // 256 elements of every row
+    static constexpr int kStageBytes = kStageK / 256 * kBoxBytes;
+    static constexpr int kRedBytes = kWarps * kGroupRows * kTok * 4;
+    static constexpr int kFactorBytes = kWarps * kWarpBlocks * kGroupRows * 4;   // twice that for NVFP4
+};
+using WideTile = Tile<4, 2>;      // 64 rows x 512 elements a stage
+using NarrowTile = Tile<8, 1>;    // 16 rows x 1024 elements a stage
+
+// Shared-memory layout of a call (host-computed; offsets and strides in bytes from a
+// 1024-byte boundary).
 struct Layout {
     int nt;                // rows of x per tile, at most kTok
-    int kc, chunks;        // elements of a weight row per stage, stages per item
-    int stages;
-    int ws, ss, xs;        // strides of a weight row, a row's scales, a row of x
-    int ring, red, total;  // the rows of x start at 0
+    int stages;            // of the weight ring, which starts at 0
+    int scale_bufs;        // items whose scales are held
+    int scale_bytes;       // of one item
+    int xs;                // stride of a row of x
+    int x, scales, red, factors, total;
 };
 
 struct Params {
@@ -62,7 +82,6 @@ struct Params {
     int rows_per_x;
     int R, N, K, E;
     const int32_t *row_ids;     // [R] or null (matrix 0)
-    const uint8_t *blocks;      // [E, N, K/2]
     const uint8_t *scales;      // [E, N, K/32] E8M0 or [E, N, K/16] E4M3
     const float *scale2;        // NVFP4: [E], or [E, 2] with SwiGLU, or null
     const float *bias;          // [E, N] or null
@@ -71,12 +90,8 @@ struct Params {
     Layout L;
 };
 
-// Strides: a weight row is an odd number of 16-byte units, so the 8 rows x 4 words of a
-// fragment load fall into 32 different banks; a row of x is 64 bytes past a multiple of
-// 128, so the two rows of a quarter-warp's 16-byte loads do.  A row's scales start at any
-// byte of their first granule.
-__host__ __device__ constexpr int weight_stride(int kc) { return ((kc / 32) | 1) * 16; }
-__host__ __device__ constexpr int scale_stride(int kc, int block) { return (kc / block + 15 + 15) / 16 * 16; }
+// A row of x is 64 bytes past a multiple of 128, so the two rows of a quarter-warp's
+// 16-byte loads fall into different banks.
 __host__ __device__ constexpr int x_row_stride(int K) { return 2 * K + ((64 - 2 * K) & 127); }
 
 // Clamped SwiGLU with the library exponential and a full division: the result may be kept
@@ -114,12 +129,18 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return r;
 }
 
-// c += A B, A 16 x 16 (weights), B 16 x 8 (x), f16 in, fp32 sums.
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+// d = A B (kNew) or d += A B, A 16 x 16 (weights), B 16 x 8 (x), f16 in, fp32 sums.
+template <bool kNew>
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    if constexpr (kNew)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
@@ -130,6 +151,11 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
 __device__ __forceinline__ uint32_t lds8(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
     return v;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -144,11 +170,19 @@ __device__ __forceinline__ float scale_pow2(float v, int e) {
     return v * __uint_as_float((uint32_t)(a + 127) << 23) * __uint_as_float((uint32_t)(b + 127) << 23);
 }
 
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void group_barrier(int group, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(2 + group), "r"(threads) : "memory");
+}
 __device__ __forceinline__ void compute_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
 
 // What a block shares besides the rows of x, the ring and the partial sums.
 struct Shared {
-    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t full[kMaxStages], empty[kMaxStages];      // weight stages
+    uint64_t scales_full[2], scales_empty[2];
     int count[kMaxExperts];         // rows per expert
     int start[kMaxExperts + 1];     // first tile of each expert
     int tok_row[kTok];              // rows r of the staged tile
@@ -273,132 +307,160 @@ __device__ __forceinline__ int stage_x(const Params &q, Shared &sh, uint8_t *xs,
     return ntok;
 }
 
-// The copies of one stage: lane l < 16 brings weight row l, lane 16 + l the granules of its
-// scales.  Every lane arrives once on `bar`.
+// The scale bytes of weight rows n0 .. n0 + rows - 1 of expert e: a run of bytes that starts
+// anywhere, copied as the 16-byte granules that hold it (the first byte lands at its
+// address modulo 16).  Called by one warp; arrives once on `full`.
 template <bool kNv>
-__device__ __forceinline__ void issue_stage(const Params &q, uint8_t *stage, uint64_t &full, int e, int n0, int k0, int kn) {
-    constexpr int kBlock = kNv ? 16 : 32;
-    const int lane = threadIdx.x & 31, row = lane & 15;
-    const uint32_t bar = ptx::smem_u32(&full);
-    if (n0 + row >= q.N) {
-        ptx::mbar_arrive(bar);
-        return;
-    }
-    const int64_t first = ((int64_t)e * q.N + n0 + row) * q.K + k0;
-    if (lane < 16) {
-        ptx::mbar_arrive_expect_tx(bar, kn / 2);
-        ptx::bulk_load(ptx::smem_u32(stage + row * q.L.ws), q.blocks + first / 2, kn / 2, bar);
-        return;
-    }
-    const int64_t a = first / kBlock, total = (int64_t)q.E * q.N * (q.K / kBlock);
-    const int64_t lo = a & ~int64_t(15);
-    int64_t hi = (a + kn / kBlock + 15) & ~int64_t(15);
-    uint8_t *dst = stage + kRows * q.L.ws + row * q.L.ss;
+__device__ __forceinline__ void issue_scales(const Params &q, uint8_t *dst, uint64_t &full, int e, int n0, int rows) {
+    const int per_row = q.K / (kNv ? 16 : 32), lane = threadIdx.x & 31;
+    const int64_t first = ((int64_t)e * q.N + n0) * per_row, last = first + (int64_t)rows * per_row;
+    const int64_t total = (int64_t)q.E * q.N * per_row, lo = first & ~int64_t(15);
+    int64_t hi = (last + 15) & ~int64_t(15);
     if (hi > total) {               // the bank's last bytes do not fill a granule: plain loads
         hi = total & ~int64_t(15);
-        for (int64_t i = max(hi, a); i < total; ++i) dst[i - lo] = __ldg(q.scales + i);
+        const int64_t i = max(hi, first) + lane;
+        if (i < total) dst[i - lo] = __ldg(q.scales + i);
+        __syncwarp();
     }
-    const uint32_t bytes = (uint32_t)(hi - lo);
-    if (!bytes) {
-        ptx::mbar_arrive(bar);
-        return;
+    if (lane == 0) {
+        const uint32_t bar = ptx::smem_u32(&full), bytes = hi > lo ? (uint32_t)(hi - lo) : 0u;
+        ptx::mbar_arrive_expect_tx(bar, bytes);
+        if (bytes) ptx::bulk_load(ptx::smem_u32(dst), q.scales + lo, bytes, bar);
     }
-    ptx::mbar_arrive_expect_tx(bar, bytes);
-    ptx::bulk_load(ptx::smem_u32(dst), q.scales + lo, bytes, bar);
 }
 
-// This warp's 32-element blocks (warp, warp + 8, ...) of one stage.  Lane (g, t): rows g and
-// g + 8 of the weights, row g of x, elements 8t .. 8t + 7 of a block (the order of k inside
-// an mma is free as long as both operands use it).  acc: rows g, g + 8 x columns 2t, 2t + 1,
-// for MXFP4 in units of 2^(e0, e1), see below.
-template <bool kNv>
-__device__ __forceinline__ void multiply_stage(const Params &q, const uint8_t *xs, const uint8_t *stage, int e, int n0, int k0,
-                                               int kn, int ntok, const int (&tok_exp)[2], float (&acc)[4]) {
-    constexpr int kBlock = kNv ? 16 : 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int blocks = kn / 32;
-    const uint32_t w0 = ptx::smem_u32(stage) + g * q.L.ws + t * 4, w1 = w0 + 8 * q.L.ws;
-    const uint32_t x0 = ptx::smem_u32(xs) + g * q.L.xs + k0 * 2 + t * 16;
-    const uint32_t sc = ptx::smem_u32(stage) + kRows * q.L.ws;
-    // the byte a row's scales start at inside their first granule
-    const auto scales_of = [&](int row) {
-        return sc + row * q.L.ss + (uint32_t)((((int64_t)e * q.N + n0 + row) * (q.K / kBlock) + k0 / kBlock) & 15);
-    };
-    const uint32_t s0 = scales_of(g), s1 = scales_of(g + 8);
-    const bool x_row = g < ntok;
+// What a warp keeps of the rows of its group while it works on an item.  Lane l stands for
+// row l when the scales become factors.
+struct RowScales {
+    uint32_t bytes;      // shared address of the row's scale bytes
+    bool valid;          // the row exists
+    bool bad;            // an invalid scale was met
+    int ref;             // MXFP4: factors are relative to this scale
+};
+
+// The factors of this warp's blocks first .. first + n - 1 (of 32 elements) of every row:
+// MXFP4 [block][g][row / 8] fp32, NVFP4 [block][half][g][row / 8] f16x2 (both halves the
+// scale), g = row % 8.
+template <class T, bool kNv>
+__device__ __forceinline__ void make_factors(uint32_t factors, RowScales &rs, int first, int n,
+                                             float (&acc)[T::kTiles][4]) {
+    const int lane = threadIdx.x & 31, g = lane & 7, r = lane >> 3;
+    const bool mine = lane < T::kGroupRows;
+    const uint32_t dst = factors + (g * 2 * T::kTiles + r) * 4;
+    constexpr int kStep = 8 * 2 * T::kTiles * 4;        // bytes of the factors of one block (half)
     if constexpr (kNv) {
-        uint32_t worst0 = 0, worst1 = 0;
-        for (int b = warp; b < blocks; b += kWarps) {
-            const uint32_t c0 = lds8(s0 + 2 * b + (t >> 1)), c1 = lds8(s1 + 2 * b + (t >> 1));
-            const uint32_t q0 = lds32(w0 + b * 16), q1 = lds32(w1 + b * 16);
-            uint4 xv = make_uint4(0u, 0u, 0u, 0u);
-            if (x_row) xv = lds128(x0 + b * 64);
-            worst0 = max(worst0, c0 & 0x7Fu);
-            worst1 = max(worst1, c1 & 0x7Fu);
-            const uint32_t both = e4m3x2_to_f16x2(c0 | (c1 << 8));
-            const uint32_t f0 = __byte_perm(both, both, 0x1010), f1 = __byte_perm(both, both, 0x3232);
-            uint32_t h0[4], h1[4];
-            e2m1x8_to_f16(q0, h0);
-            e2m1x8_to_f16(q1, h1);
+        uint32_t worst = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                h0[i] = mul_f16x2(h0[i], f0);
-                h1[i] = mul_f16x2(h1[i], f1);
+        for (int i = 0; i < kWarpBlocks; ++i) {
+            uint32_t c0 = 0, c1 = 0;
+            if (rs.valid && i < n) {
+                c0 = lds8(rs.bytes + 2 * (first + i));
+                c1 = lds8(rs.bytes + 2 * (first + i) + 1);
             }
-            mma_f16(acc, h0[0], h1[0], h0[1], h1[1], xv.x, xv.y);
-            mma_f16(acc, h0[2], h1[2], h0[3], h1[3], xv.z, xv.w);
+            worst = max(worst, max(c0 & 0x7Fu, c1 & 0x7Fu));
+            const uint32_t both = e4m3x2_to_f16x2(c0 | (c1 << 8));
+            if (mine) {
+                sts32(dst + 2 * i * kStep, __byte_perm(both, both, 0x1010));
+                sts32(dst + (2 * i + 1) * kStep, __byte_perm(both, both, 0x3232));
+            }
         }
-        if ((worst0 == 0x7Fu && n0 + g < q.N) || (worst1 == 0x7Fu && n0 + g + 8 < q.N))
-            raise_device_error(MOE_DEVERR_BAD_SCALE);
+        rs.bad |= worst == 0x7Fu;
     } else {
-        // the largest scale of each row in this warp's blocks: two lanes a row
-        uint32_t top = 0;
-        if (n0 + (lane >> 1) < q.N) {
-            const uint32_t s = scales_of(lane >> 1);
-            for (int b = warp + kWarps * (lane & 1); b < blocks; b += 2 * kWarps) top = max(top, lds8(s + b));
+        int s[kWarpBlocks], top = 0;
+#pragma unroll
+        for (int i = 0; i < kWarpBlocks; ++i) {
+            s[i] = rs.valid && i < n ? (int)lds8(rs.bytes + first + i) : 0;
+            top = max(top, s[i]);
         }
-        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        if (top == 255u) raise_device_error(MOE_DEVERR_BAD_SCALE);
-        const int top0 = (int)__shfl_sync(0xFFFFFFFFu, top, 2 * g), top1 = (int)__shfl_sync(0xFFFFFFFFu, top, 2 * (g + 8));
-        // scale factors 2^(s - top + 64)
-        const int d0 = 191 - top0, d1 = 191 - top1;
-        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int b = warp; b < blocks; b += kWarps) {
-            const int c0 = (int)lds8(s0 + b), c1 = (int)lds8(s1 + b);
-            const uint32_t q0 = lds32(w0 + b * 16), q1 = lds32(w1 + b * 16);
-            uint4 xv = make_uint4(0u, 0u, 0u, 0u);
-            if (x_row) xv = lds128(x0 + b * 64);
+        rs.bad |= top == 255;
+        if (rs.ref < 0) rs.ref = top;
+        // Factors stay below 2^64: when a later stage brings larger scales, the sums are
+        // brought to the new reference.
+        const int up = top > rs.ref + 64 ? top - rs.ref : 0;
+        if (__any_sync(0xFFFFFFFFu, up)) {
+            rs.ref += up;
+#pragma unroll
+            for (int m = 0; m < T::kTiles; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int by = __shfl_sync(0xFFFFFFFFu, up, (lane >> 2) + 8 * h + 16 * m);
+                    acc[m][2 * h] = scale_pow2(acc[m][2 * h], -by);
+                    acc[m][2 * h + 1] = scale_pow2(acc[m][2 * h + 1], -by);
+                }
+        }
+        if (mine) {
+#pragma unroll
+            for (int i = 0; i < kWarpBlocks; ++i) sts32(dst + i * kStep, (uint32_t)max(s[i] - rs.ref + 127, 0) << 23);
+        }
+    }
+    __syncwarp();
+}
+
+// This warp's n (at most kWarpBlocks) blocks of one stage.  Lane (g, t): rows g, g + 8, ...
+// of the group, row g of x, elements 8t .. 8t + 7 of a block (the order of k inside an mma
+// is free as long as both operands use it).  Swizzled boxes: the 16-byte unit u of row r
+// lies at unit u ^ (r % 8), and a block is a unit.  acc: rows g, g + 8 of tile m x columns
+// 2t, 2t + 1.
+template <class T, bool kNv>
+__device__ __forceinline__ void multiply_blocks(uint32_t weights, uint32_t x, uint32_t factors, int unit, int n,
+                                                float (&acc)[T::kTiles][4]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < kWarpBlocks; ++i) {
+        if (i >= n) break;
+        const uint32_t w = weights + (((unit + i) ^ g) << 4);
+        const uint4 xv = lds128(x + i * 64);
+        uint32_t f[2 * T::kTiles];
+        const uint32_t fa = factors + (kNv ? (2 * i + (t >> 1)) * 8 + g : i * 8 + g) * 8 * T::kTiles;
+        if constexpr (T::kTiles == 2) {
+            const uint4 v = lds128(fa);
+            f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+        } else {
+            const uint2 v = lds64(fa);
+            f[0] = v.x, f[1] = v.y;
+        }
+#pragma unroll
+        for (int m = 0; m < T::kTiles; ++m) {
             uint32_t h0[4], h1[4];
-            e2m1x8_to_f16(q0, h0);
-            e2m1x8_to_f16(q1, h1);
-            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma_f16(c, h0[0], h1[0], h0[1], h1[1], xv.x, xv.y);
-            mma_f16(c, h0[2], h1[2], h0[3], h1[3], xv.z, xv.w);
-            const float f0 = __uint_as_float((uint32_t)max(c0 + d0, 0) << 23);
-            const float f1 = __uint_as_float((uint32_t)max(c1 + d1, 0) << 23);
-            part[0] = fmaf(c[0], f0, part[0]);
-            part[1] = fmaf(c[1], f0, part[1]);
-            part[2] = fmaf(c[2], f1, part[2]);
-            part[3] = fmaf(c[3], f1, part[3]);
+            e2m1x8_to_f16(lds32(w + m * 2048), h0);
+            e2m1x8_to_f16(lds32(w + m * 2048 + 1024), h1);
+            if constexpr (kNv) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    h0[j] = mul_f16x2(h0[j], f[2 * m]);
+                    h1[j] = mul_f16x2(h1[j], f[2 * m + 1]);
+                }
+                mma_f16<false>(acc[m], h0[0], h1[0], h0[1], h1[1], xv.x, xv.y);
+                mma_f16<false>(acc[m], h0[2], h1[2], h0[3], h1[3], xv.z, xv.w);
+            } else {
+                float c[4];
+                mma_f16<true>(c, h0[0], h1[0], h0[1], h1[1], xv.x, xv.y);
+                mma_f16<false>(c, h0[2], h1[2], h0[3], h1[3], xv.z, xv.w);
+                const float f0 = __uint_as_float(f[2 * m]), f1 = __uint_as_float(f[2 * m + 1]);
+                acc[m][0] = fmaf(c[0], f0, acc[m][0]);
+                acc[m][1] = fmaf(c[1], f0, acc[m][1]);
+                acc[m][2] = fmaf(c[2], f1, acc[m][2]);
+                acc[m][3] = fmaf(c[3], f1, acc[m][3]);
+            }
         }
-        const float nan = __uint_as_float(0x7FC00000u);
-        const int e0 = top0 - 127 - 64, e1 = top1 - 127 - 64;
-        acc[0] += top0 == 255 ? nan : scale_pow2(part[0], e0 + tok_exp[0]);
-        acc[1] += top0 == 255 ? nan : scale_pow2(part[1], e0 + tok_exp[1]);
-        acc[2] += top1 == 255 ? nan : scale_pow2(part[2], e1 + tok_exp[0]);
-        acc[3] += top1 == 255 ? nan : scale_pow2(part[3], e1 + tok_exp[1]);
     }
 }
 
-template <class X, class Out, bool kNv, bool kSwiGlu>
-__global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const __grid_constant__ Params q) {
-    extern __shared__ __align__(128) uint8_t sm[];
+template <class T, class X, class Out, bool kNv, bool kSwiGlu>
+__global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const __grid_constant__ CUtensorMap weights,
+                                                             const __grid_constant__ Params q) {
+    extern __shared__ uint8_t dynamic_smem[];
     __shared__ Shared sh;
+    uint8_t *sm = dynamic_smem + ((1024u - (ptx::smem_u32(dynamic_smem) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < q.L.stages; ++i) {
-            ptx::mbar_init(ptx::smem_u32(&sh.full[i]), 32);
+            ptx::mbar_init(ptx::smem_u32(&sh.full[i]), 1);
             ptx::mbar_init(ptx::smem_u32(&sh.empty[i]), kWarps);
+        }
+        for (int i = 0; i < q.L.scale_bufs; ++i) {
+            ptx::mbar_init(ptx::smem_u32(&sh.scales_full[i]), 1);
+            ptx::mbar_init(ptx::smem_u32(&sh.scales_empty[i]), kWarps);
         }
         ptx::fence_mbarrier_init();
         sh.failed = 0;
@@ -406,50 +468,90 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const __grid_consta
     pdl_wait();
     pdl_trigger();
     count_tiles(q, sh);
-    const int n_tiles = (q.N + kRows - 1) / kRows;
+    const int n_tiles = (q.N + T::kRows - 1) / T::kRows, chunks = (q.K + T::kStageK - 1) / T::kStageK;
     const int64_t items = (int64_t)sh.start[q.E] * n_tiles;
     const int beg = (int)(items * blockIdx.x / gridDim.x), end = (int)(items * (blockIdx.x + 1) / gridDim.x);
-    const int stage_bytes = kRows * (q.L.ws + q.L.ss);
-    uint8_t *ring = sm + q.L.ring;
-    int stage = 0, e = 0;
-    uint32_t phase = 0;
+    int slot = beg / n_tiles, tile = beg - slot * n_tiles, e = 0;
+    int stage = 0, sbuf = 0;
+    uint32_t phase = 0, sphase = 0;
 
     if (warp == kWarps) {
         for (int it = beg; it < end; ++it) {
-            const int slot = it / n_tiles, n0 = (it - slot * n_tiles) * kRows;
             while (sh.start[e + 1] <= slot) ++e;
-            for (int c = 0; c < q.L.chunks; ++c) {
-                const int k0 = c * q.L.kc, kn = min(q.L.kc, q.K - k0);
+            const int n0 = tile * T::kRows;
+            for (int c = 0; c < chunks; ++c) {
                 wait_or_fail(sh, sh.empty[stage], phase ^ 1u);
                 __syncwarp();
-                issue_stage<kNv>(q, ring + stage * stage_bytes, sh.full[stage], e, n0, k0, kn);
+                if (lane == 0) {
+                    const uint32_t bar = ptx::smem_u32(&sh.full[stage]);
+                    const int units = min(T::kStageK, q.K - c * T::kStageK);
+                    const int boxes = (units + 255) / 256;
+                    ptx::mbar_arrive_expect_tx(bar, boxes * T::kBoxBytes);
+                    for (int b = 0; b < boxes; ++b)
+                        ptx::tma_load_2d(ptx::smem_u32(sm + stage * T::kStageBytes + b * T::kBoxBytes), &weights,
+                                         c * (T::kStageK / 2) + b * 128, e * q.N + n0, bar);
+                }
+                if (c == 0) {
+                    wait_or_fail(sh, sh.scales_empty[sbuf], sphase ^ 1u);
+                    __syncwarp();
+                    issue_scales<kNv>(q, sm + q.L.scales + sbuf * q.L.scale_bytes, sh.scales_full[sbuf], e, n0,
+                                      min(T::kRows, q.N - n0));
+                    if (++sbuf == q.L.scale_bufs) {
+                        sbuf = 0;
+                        sphase ^= 1u;
+                    }
+                }
                 if (++stage == q.L.stages) {
                     stage = 0;
                     phase ^= 1u;
                 }
             }
+            if (++tile == n_tiles) {
+                tile = 0;
+                ++slot;
+            }
         }
         return;
     }
 
-    float *red = reinterpret_cast<float *>(sm + q.L.red);     // [2][kWarps][kRows][kTok]
+    const int group = warp / T::kSplit, part = warp % T::kSplit, g = lane >> 2, t = lane & 3;
+    const int per_row = q.K / (kNv ? 16 : 32);
     const int n_out = kSwiGlu ? q.N / 2 : q.N;
+    const uint32_t ring = ptx::smem_u32(sm) + part / 2 * T::kBoxBytes + (group * T::kGroupRows + g) * 128 + t * 4;
+    const uint32_t factors = ptx::smem_u32(sm + q.L.factors) + warp * (kNv ? 2 : 1) * (T::kFactorBytes / kWarps);
+    float *red = reinterpret_cast<float *>(sm + q.L.red) + group * T::kSplit * T::kGroupRows * kTok;
     int staged = -1, ntok = 0;
     int tok_exp[2] = {0, 0};
+    uint32_t x0 = 0;
     for (int it = beg; it < end; ++it) {
-        const int slot = it / n_tiles, n0 = (it - slot * n_tiles) * kRows;
+        const int n0 = tile * T::kRows + group * T::kGroupRows;      // this group's first row
         if (slot != staged) {
             while (sh.start[e + 1] <= slot) ++e;
-            ntok = stage_x<X>(q, sh, sm, e, slot);
+            ntok = stage_x<X>(q, sh, sm + q.L.x, e, slot);
             staged = slot;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) tok_exp[i] = 2 * (lane & 3) + i < ntok ? sh.tok_exp[2 * (lane & 3) + i] : 0;
+            for (int i = 0; i < 2; ++i) tok_exp[i] = 2 * t + i < ntok ? sh.tok_exp[2 * t + i] : 0;
+            // columns past the staged rows repeat the last one (and are not stored)
+            x0 = ptx::smem_u32(sm + q.L.x) + min(g, ntok - 1) * q.L.xs + part * (kWarpBlocks * 64) + t * 16;
         }
-        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int c = 0; c < q.L.chunks; ++c) {
-            const int k0 = c * q.L.kc, kn = min(q.L.kc, q.K - k0);
+        RowScales rs;
+        rs.valid = lane < T::kGroupRows && n0 + lane < q.N;
+        rs.bad = false;
+        rs.ref = -1;
+        rs.bytes = ptx::smem_u32(sm + q.L.scales) + sbuf * q.L.scale_bytes +
+                   ((uint32_t)(e * q.N + tile * T::kRows) * (uint32_t)per_row & 15u) +
+                   (group * T::kGroupRows + lane) * per_row;
+        wait_or_fail(sh, sh.scales_full[sbuf], sphase);
+        float acc[T::kTiles][4];
+#pragma unroll
+        for (int m = 0; m < T::kTiles; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.0f;
+        for (int c = 0; c < chunks; ++c) {
+            const int first = c * (T::kStageK / 32) + part * kWarpBlocks, n = min(kWarpBlocks, q.K / 32 - first);
+            if (n > 0) make_factors<T, kNv>(factors, rs, first, n, acc);
             wait_or_fail(sh, sh.full[stage], phase);
-            multiply_stage<kNv>(q, sm, ring + stage * stage_bytes, e, n0, k0, kn, ntok, tok_exp, acc);
+            if (n > 0)
+                multiply_blocks<T, kNv>(ring + stage * T::kStageBytes, x0 + c * (T::kStageK * 2), factors,
+                                        (part & 1) * kWarpBlocks, n, acc);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.empty[stage]));
             if (++stage == q.L.stages) {
@@ -457,17 +559,37 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const __grid_consta
                 phase ^= 1u;
             }
         }
-        // join the warps' sums; the other half of `red` was last read before this barrier
-        float *part = red + (it & 1) * kWarps * kRows * kTok;
-        float *mine = part + warp * kRows * kTok + (lane >> 2) * kTok + 2 * (lane & 3);
-        *reinterpret_cast<float2 *>(mine) = make_float2(acc[0], acc[1]);
-        *reinterpret_cast<float2 *>(mine + 8 * kTok) = make_float2(acc[2], acc[3]);
-        compute_barrier();
-        if (tid < kRows * kTok) {
-            const int row = tid / kTok, tok = tid % kTok, n = n0 + row;
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.scales_empty[sbuf]));
+        if (++sbuf == q.L.scale_bufs) {
+            sbuf = 0;
+            sphase ^= 1u;
+        }
+        if (rs.bad && rs.valid) raise_device_error(MOE_DEVERR_BAD_SCALE);
+        if constexpr (!kNv) {
+            // from the reference scales and the staged x to the true scale; a row with an invalid scale is NaN
+            const int row_e = rs.bad ? 1 << 20 : rs.ref - 127;
+#pragma unroll
+            for (int m = 0; m < T::kTiles; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int re = __shfl_sync(0xFFFFFFFFu, row_e, g + 8 * (i >> 1) + 16 * m);
+                    acc[m][i] = re == 1 << 20 ? __uint_as_float(0x7FC00000u) : scale_pow2(acc[m][i], re + tok_exp[i & 1]);
+                }
+        }
+        // join the warps' sums
+        group_barrier(group, 32 * T::kSplit);          // the previous item's are read
+#pragma unroll
+        for (int m = 0; m < T::kTiles; ++m) {
+            float *mine = red + (part * T::kGroupRows + 16 * m + g) * kTok + 2 * t;
+            *reinterpret_cast<float2 *>(mine) = make_float2(acc[m][0], acc[m][1]);
+            *reinterpret_cast<float2 *>(mine + 8 * kTok) = make_float2(acc[m][2], acc[m][3]);
+        }
+        group_barrier(group, 32 * T::kSplit);
+        for (int o = part * 32 + lane; o < T::kGroupRows * kTok; o += 32 * T::kSplit) {
+            const int row = o / kTok, tok = o % kTok, n = n0 + row;
             float v = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) v += part[w * kRows * kTok + tid];
+            for (int w = 0; w < T::kSplit; ++w) v += red[w * T::kGroupRows * kTok + o];
             const bool live = n < q.N && tok < ntok;
             if (live) {
                 if constexpr (kNv) {
@@ -485,9 +607,15 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const __grid_consta
                 static_cast<Out *>(q.out)[(int64_t)sh.tok_row[tok] * n_out + n] = f32_to_elem<Out>(v);
             }
         }
+        if (++tile == n_tiles) {
+            tile = 0;
+            ++slot;
+        }
     }
     if (sh.failed) {                 // a wait gave up: the copies still under way, once more with a limit
         for (int i = 0; i < q.L.stages; ++i) ptx::mbar_wait(ptx::smem_u32(&sh.full[i]), i < stage ? phase : phase ^ 1u);
+        for (int i = 0; i < q.L.scale_bufs; ++i)
+            ptx::mbar_wait(ptx::smem_u32(&sh.scales_full[i]), i < sbuf ? sphase : sphase ^ 1u);
     }
 }
 

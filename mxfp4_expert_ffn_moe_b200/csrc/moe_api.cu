@@ -807,47 +807,84 @@ int sum_rows(const void *rows, int rows_dtype, int64_t rows_stride, int64_t T, i
 }
 
 // ---- products of a few rows with 4-bit weights ----------------------------------
-// Shared memory of a call.  Rows of x per tile: 8, or as many as fit beside two stages.
-// Stages: what keeps two CTAs on an SM, 2 at least and 4 at most.  0 stages: does not fit.
+// Shared memory of a call.  Rows of x per tile: 8, or as many as fit beside two stages and
+// one buffer of scales.  Stages and scale buffers: what keeps two CTAs on an SM where that
+// fits, 2 to 4 stages and 1 or 2 buffers.  0 stages: does not fit.
+template <class T>
 moe::mv::Layout matvec_layout(int64_t R, int64_t K, int block, int limit) {
     namespace mv = moe::mv;
     mv::Layout L{};
-    L.chunks = (int)moe::ceil_div(K, mv::kStageK);
-    L.kc = (int)(moe::ceil_div(moe::ceil_div(K, L.chunks), 32) * 32);
-    L.chunks = (int)moe::ceil_div(K, L.kc);
-    L.ws = mv::weight_stride(L.kc);
-    L.ss = mv::scale_stride(L.kc, block);
     L.xs = mv::x_row_stride((int)K);
-    const int stage = mv::kRows * (L.ws + L.ss), red = 2 * mv::kWarps * mv::kRows * mv::kTok * 4;
-    const int fixed = red + (int)sizeof(mv::Shared) + 1024;       // 1 KB is the system's
-    const int64_t fit = ((int64_t)limit - fixed - 2 * stage) / L.xs;
+    L.scale_bytes = (T::kRows * (int)(K / block) + 15 + 127) / 128 * 128;
+    const int factors = T::kFactorBytes * (block == 16 ? 2 : 1);
+    // the system's 1 KB, the way to a 1024-byte boundary, and rounding
+    const int fixed = T::kRedBytes + factors + (int)sizeof(mv::Shared) + 1024 + 1024 + 128;
+    const int64_t fit = ((int64_t)limit - fixed - L.scale_bytes - 2 * T::kStageBytes) / L.xs;
     L.nt = (int)std::min<int64_t>(std::min<int64_t>(mv::kTok, R), fit);
     if (L.nt < 1) return L;
     const int x_bytes = (L.nt * L.xs + 127) / 128 * 128;
-    L.stages = (limit / 2 - fixed - x_bytes) / stage;
-    if (L.stages < 2) L.stages = (limit - fixed - x_bytes) / stage;
-    L.stages = std::max(2, std::min(L.stages, mv::kMaxStages));
-    L.ring = x_bytes;
-    L.red = L.ring + L.stages * stage;
-    L.total = L.red + red;
+    for (const int room : {limit / 2, limit}) {
+        for (L.scale_bufs = 2; L.scale_bufs >= 1; --L.scale_bufs) {
+            L.stages = std::min((room - fixed - x_bytes - L.scale_bufs * L.scale_bytes) / T::kStageBytes, mv::kMaxStages);
+            if (L.stages >= 2) break;
+        }
+        if (L.stages >= 2) break;
+    }
+    L.x = L.stages * T::kStageBytes;
+    L.scales = L.x + x_bytes;
+    L.red = L.scales + L.scale_bufs * L.scale_bytes;
+    L.factors = L.red + T::kRedBytes;
+    L.total = L.factors + factors + 1024;
     return L;
 }
 
+// packed 4-bit codes [E * N, K/2] bytes: box of 128 bytes (128-byte swizzle) x `rows` rows.
+bool make_matvec_map(CUtensorMap *m, const void *ptr, int64_t rows_total, int64_t K, int rows) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)(K / 2), (cuuint64_t)rows_total};
+    cuuint64_t strides[1] = {(cuuint64_t)(K / 2)};
+    cuuint32_t box[2] = {128, (cuuint32_t)rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tiles of x over all experts, at most: every row alone, or every expert's last tile ragged.
+int64_t matvec_slots(const moe::mv::Params &q, int nt) {
+    return q.row_ids ? std::min<int64_t>(q.R, q.E + q.R / nt) : moe::ceil_div(q.R, nt);
+}
+
+template <class T, class X, class Out, bool kNv, bool kSwiGlu>
+int launch_matvec_tile(moe::mv::Params q, const uint8_t *blocks, int optin, cudaStream_t s) {
+    namespace mv = moe::mv;
+    q.L = matvec_layout<T>(q.R, q.K, kNv ? 16 : 32, optin);
+    if (q.L.stages < 2) return MOE_ERR_UNSUPPORTED;
+    CUtensorMap map;
+    if (!make_matvec_map(&map, blocks, (int64_t)q.E * q.N, q.K, T::kRows)) return MOE_ERR_CUDA;
+    auto kernel = mv::matvec_kernel<T, X, Out, kNv, kSwiGlu>;
+    if (!ensure_smem_attr(reinterpret_cast<const void *>(kernel), q.L.total)) return MOE_ERR_CUDA;
+    const int per_sm = 2 * (q.L.total + (int)sizeof(mv::Shared) + 1024) <= optin + 1024 ? 2 : 1;
+    const int64_t grid = std::min<int64_t>(matvec_slots(q, q.L.nt) * moe::ceil_div(q.N, T::kRows),
+                                           (int64_t)sm_count() * per_sm);
+    StageScope scope(kSwiGlu ? MOE_STAGE_GATE_UP : MOE_STAGE_DOWN, s);
+    launch_pdl(kernel, dim3((unsigned)grid), dim3(mv::kThreads), q.L.total, s, map, q);
+    return launch_check();
+}
+
+#ifndef MOE_WIDE_ITEMS
+#define MOE_WIDE_ITEMS 4
+#endif
 template <class X, class Out, bool kNv, bool kSwiGlu>
-int launch_matvec(moe::mv::Params q, cudaStream_t s) {
+int launch_matvec(const moe::mv::Params &q, const uint8_t *blocks, cudaStream_t s) {
     namespace mv = moe::mv;
     const int optin = max_smem_optin();
-    q.L = matvec_layout(q.R, q.K, kNv ? 16 : 32, optin);
-    if (q.L.stages < 2) return MOE_ERR_UNSUPPORTED;
-    auto kernel = mv::matvec_kernel<X, Out, kNv, kSwiGlu>;
-    if (!ensure_smem_attr(reinterpret_cast<const void *>(kernel), q.L.total)) return MOE_ERR_CUDA;
-    // at most every row alone, or every expert's last tile ragged
-    const int64_t slots = q.row_ids ? std::min<int64_t>(q.R, q.E + q.R / q.L.nt) : moe::ceil_div(q.R, q.L.nt);
-    const int per_sm = 2 * (q.L.total + (int)sizeof(mv::Shared) + 1024) <= optin + 1024 ? 2 : 1;
-    const int64_t grid = std::min<int64_t>(slots * moe::ceil_div(q.N, mv::kRows), (int64_t)sm_count() * per_sm);
-    StageScope scope(kSwiGlu ? MOE_STAGE_GATE_UP : MOE_STAGE_DOWN, s);
-    launch_pdl(kernel, dim3((unsigned)grid), dim3(mv::kThreads), q.L.total, s, q);
-    return launch_check();
+    const bool wide = matvec_slots(q, std::min(q.R, mv::kTok)) * moe::ceil_div(q.N, mv::WideTile::kRows) >=
+                          MOE_WIDE_ITEMS * sm_count() &&
+                      matvec_layout<mv::WideTile>(q.R, q.K, kNv ? 16 : 32, optin).stages >= 2;
+    return wide ? launch_matvec_tile<mv::WideTile, X, Out, kNv, kSwiGlu>(q, blocks, optin, s)
+                : launch_matvec_tile<mv::NarrowTile, X, Out, kNv, kSwiGlu>(q, blocks, optin, s);
 }
 
 template <bool kNv>
@@ -861,15 +898,15 @@ int matvec(const void *x, int x_dtype, int64_t x_stride, int rows_per_x, int64_t
         (swiglu && N % 2 != 0))
         return MOE_ERR_INVALID_ARG;
     if (!dtype_size(x_dtype) || !dtype_size(out_dtype)) return MOE_ERR_INVALID_ARG;
-    if (R > MOE_MATVEC_MAX_ROWS || E > moe::mv::kMaxExperts || N > (1 << 24) || K > (1 << 16)) return MOE_ERR_UNSUPPORTED;
+    if (R > MOE_MATVEC_MAX_ROWS || E > moe::mv::kMaxExperts || N > (1 << 24) || K > (1 << 16) || E * N >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
     if (x_dtype == MOE_DTYPE_F32 || (out_dtype != x_dtype && out_dtype != MOE_DTYPE_F32)) return MOE_ERR_UNSUPPORTED;
     if (!aligned(x, 16) || (x_stride % 8) != 0 || !aligned(blocks, 16) || !aligned(scales, 16) || !aligned(row_ids, 4) ||
         !aligned(scale2, 4) || !aligned(bias, 4) || !aligned(out, dtype_size(out_dtype)))
         return MOE_ERR_INVALID_ARG;
     const moe::mv::Params q{x,      x_stride, rows_per_x, (int)R, (int)N, (int)K, (int)E, row_ids,
-                            blocks, scales,   scale2,     bias,   alpha,  limit,  out,    {}};
+                            scales, scale2,   bias,       alpha,  limit,  out,    {}};
 #define MOE_MATVEC(X, OUT) \
-    return swiglu ? launch_matvec<X, OUT, kNv, true>(q, s) : launch_matvec<X, OUT, kNv, false>(q, s)
+    return swiglu ? launch_matvec<X, OUT, kNv, true>(q, blocks, s) : launch_matvec<X, OUT, kNv, false>(q, blocks, s)
     if (x_dtype == MOE_DTYPE_BF16) {
         if (out_dtype == MOE_DTYPE_F32) MOE_MATVEC(__nv_bfloat16, float);
         MOE_MATVEC(__nv_bfloat16, __nv_bfloat16);
