@@ -454,8 +454,8 @@ _DTYPE_CODES = {}
 
 
 def _dtype_code(dtype, name):
-    import torch
     if not _DTYPE_CODES:
+        import torch
         _DTYPE_CODES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
     code = _DTYPE_CODES.get(dtype)
     if code is None:
@@ -466,27 +466,33 @@ def _dtype_code(dtype, name):
 class _Call:
     """Argument marshalling of one call: every tensor on the current CUDA device, outputs
     allocated for the stream the call runs on, and tensors used on a stream other than
-    the current one kept from the allocator until that stream has run the call."""
+    the current one kept from the allocator until that stream has run the call.  A decode
+    step makes many such calls, so this is kept short: raw stream and device handles, one
+    pass over each tensor's properties."""
+
+    __slots__ = ("torch", "device", "side", "stream")
 
     def __init__(self, like, stream):
         import torch
         self.torch = torch
-        self.device = like.device
-        if not like.is_cuda or like.device.index != torch.cuda.current_device():
+        self.device = like.get_device()
+        if self.device < 0 or self.device != torch._C._cuda_getDevice():
             raise ValueError(f"expected tensors on the current CUDA device, got one on {like.device}")
-        current = torch.cuda.current_stream()
-        self.side = stream if stream is not None and stream != current else None
-        self.stream = ctypes.c_void_p((stream or current).cuda_stream)
+        self.side = None
+        self.stream = torch._C._cuda_getCurrentRawStream(self.device)
+        if stream is not None and stream.cuda_stream != self.stream:
+            self.side = stream
+            self.stream = stream.cuda_stream
 
-    def empty(self, shape, dtype):
+    def empty(self, like, shape, dtype):
         if self.side is None:
-            return self.torch.empty(shape, dtype=dtype, device=self.device)
+            return like.new_empty(shape, dtype=dtype)
         with self.torch.cuda.stream(self.side):
-            return self.torch.empty(shape, dtype=dtype, device=self.device)
+            return like.new_empty(shape, dtype=dtype)
 
     def _use(self, t, name):
-        if t.device != self.device:
-            raise ValueError(f"{name}: on {t.device}, expected {self.device}")
+        if t.get_device() != self.device:
+            raise ValueError(f"{name}: on {t.device}, expected cuda:{self.device}")
         if self.side is not None:
             t.record_stream(self.side)
 
@@ -494,7 +500,7 @@ class _Call:
         """Contiguous tensor of `numel` elements (None stays None)."""
         if t is None:
             return None
-        if t.dtype != dtype or t.numel() != numel or not t.is_contiguous():
+        if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous():
             raise ValueError(f"{name}: expected a contiguous {dtype} tensor of {numel} elements, got "
                              f"{t.dtype} {tuple(t.shape)} (contiguous={t.is_contiguous()})")
         self._use(t, name)
@@ -505,7 +511,7 @@ class _Call:
         if t is None:
             return None, 0, 0
         code = _dtype_code(t.dtype, name)
-        if tuple(t.shape) != shape or (dtype is not None and t.dtype != dtype) or (shape[1] > 1 and t.stride(1) != 1):
+        if t.shape != shape or (dtype is not None and t.dtype is not dtype) or (shape[1] > 1 and t.stride(1) != 1):
             raise ValueError(f"{name}: expected {shape}{'' if dtype is None else f' of {dtype}'} with contiguous rows, "
                              f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
         self._use(t, name)
@@ -522,7 +528,7 @@ def moe_dispatch_rows(x, pair_rows, k: int, weights=None, n_rows: Optional[int] 
     c = _Call(x, stream)
     T, H = x.shape
     if rows is None:
-        rows = c.empty((T * k if n_rows is None else n_rows, H), dtype or x.dtype)
+        rows = c.empty(x, (T * k if n_rows is None else n_rows, H), dtype or x.dtype)
     xp, xd, xs = c.rows(x, "x", (T, H))
     rp, rd, rs = c.rows(rows, "rows", (rows.shape[0], H), dtype)
     _check("moe_dispatch_rows", load_library().moe_dispatch_rows(
@@ -539,9 +545,9 @@ def moe_dispatch_rows_backward(drows, pair_rows, T: int, k: int, weights=None, x
     c = _Call(drows, stream)
     R, H = drows.shape
     if dx is None:
-        dx = c.empty((T, H), dtype or (drows.dtype if x is None else x.dtype))
+        dx = c.empty(drows, (T, H), dtype or (drows.dtype if x is None else x.dtype))
     if x is not None and dweights is None:
-        dweights = c.empty((T, k), c.torch.float32)
+        dweights = c.empty(drows, (T, k), c.torch.float32)
     rp, rd, rs = c.rows(drows, "drows", (R, H))
     dp, dd, ds = c.rows(dx, "dx", (T, H), dtype)
     xp, _, xs = c.rows(x, "x", (T, H), dx.dtype)
@@ -560,7 +566,7 @@ def moe_combine_rows(rows, pair_rows, T: int, k: int, weights=None, dtype=None, 
     c = _Call(rows, stream)
     R, H = rows.shape
     if out is None:
-        out = c.empty((T, H), dtype or rows.dtype)
+        out = c.empty(rows, (T, H), dtype or rows.dtype)
     rp, rd, rs = c.rows(rows, "rows", (R, H))
     op, od, os_ = c.rows(out, "out", (T, H), dtype)
     _check("moe_combine_rows", load_library().moe_combine_rows(
@@ -580,10 +586,10 @@ def moe_combine_rows_backward(dout, pair_rows, k: int, weights=None, y_rows=None
     T, H = dout.shape
     if drows is None:
         n = y_rows.shape[0] if y_rows is not None else T * k if n_rows is None else n_rows
-        drows = c.empty((n, H), dtype or (dout.dtype if y_rows is None else y_rows.dtype))
+        drows = c.empty(dout, (n, H), dtype or (dout.dtype if y_rows is None else y_rows.dtype))
     R = drows.shape[0]
     if y_rows is not None and dweights is None:
-        dweights = c.empty((T, k), c.torch.float32)
+        dweights = c.empty(dout, (T, k), c.torch.float32)
     op, od, os_ = c.rows(dout, "dout", (T, H))
     dp, dd, ds = c.rows(drows, "drows", (R, H), dtype)
     yp, _, ys = c.rows(y_rows, "y_rows", (R, H), drows.dtype)
@@ -600,7 +606,7 @@ def moe_route_backward(dweights, ids, weights, E: int, dlogits=None, stream=None
     c = _Call(dweights, stream)
     T, k = dweights.shape
     if dlogits is None:
-        dlogits = c.empty((T, E), c.torch.float32)
+        dlogits = c.empty(dweights, (T, E), c.torch.float32)
     _check("moe_route_backward", load_library().moe_route_backward(
         c.flat(dweights, c.torch.float32, "dweights", T * k), c.flat(ids, c.torch.int32, "ids", T * k),
         c.flat(weights, c.torch.float32, "weights", T * k), T, int(E), k,
@@ -621,7 +627,7 @@ def _matvec(name, block, x, blocks, scales, scale2, bias, row_ids, rows_per_x, s
         raise ValueError(f"{name}: {R} rows at {rows_per_x} per row of x do not make the {Tx} rows of x")
     shape = (R, N // 2 if swiglu else N)
     if out is None:
-        out = c.empty(shape, out_dtype or x.dtype)
+        out = c.empty(x, shape, out_dtype or x.dtype)
     if not out.is_contiguous():
         raise ValueError("out: expected a contiguous tensor")
     xp, xd, xs = c.rows(x, "x", (Tx, K))

@@ -43,16 +43,16 @@ namespace moe {
 namespace mv {
 
 constexpr int kTok = 8;                // rows of x of an item (mma N)
-constexpr int kWarps = 8;              // computing warps; one more issues the copies
-constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kMaxStages = 4;
 constexpr int kMaxExperts = 256;
 constexpr int kWarpBlocks = 4;         // 32-element blocks of a warp in one stage
 
-// kSplit warps over the K of a group of 16 * kTiles weight rows.
-template <int kSplit_, int kTiles_>
+// kWarps computing warps (one more issues the copies), kSplit of them over the K of each
+// group of 16 * kTiles weight rows; kBlocksPerSm such blocks on an SM.
+template <int kWarps_, int kSplit_, int kTiles_, int kBlocksPerSm_>
 struct Tile {
-    static constexpr int kSplit = kSplit_, kTiles = kTiles_;
+    static constexpr int kWarps = kWarps_, kSplit = kSplit_, kTiles = kTiles_, kBlocksPerSm = kBlocksPerSm_;
+    static constexpr int kThreads = 32 * (kWarps + 1);
     static constexpr int kGroups = kWarps / kSplit;
     static constexpr int kGroupRows = 16 * kTiles;
     static constexpr int kRows = kGroups * kGroupRows;           // weight rows of an item
@@ -62,8 +62,11 @@ struct Tile {
     static constexpr int kRedBytes = kWarps * kGroupRows * kTok * 4;
     static constexpr int kFactorBytes = kWarps * kWarpBlocks * kGroupRows * 4;   // twice that for NVFP4
 };
-using WideTile = Tile<4, 2>;      // 64 rows x 512 elements a stage
-using NarrowTile = Tile<8, 1>;    // 16 rows x 1024 elements a stage
+#ifndef MOE_WIDE
+#define MOE_WIDE 16, 4, 2, 1
+#endif
+using WideTile = Tile<MOE_WIDE>;        // 128 rows x 512 elements a stage
+using NarrowTile = Tile<8, 8, 1, 2>;    // 16 rows x 1024 elements a stage
 
 // Shared-memory layout of a call (host-computed; offsets and strides in bytes from a
 // 1024-byte boundary).
@@ -143,6 +146,8 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Loads of shared memory in program order with the barriers around them, but free to move
+// past arithmetic.
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
@@ -177,7 +182,10 @@ __device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
 __device__ __forceinline__ void group_barrier(int group, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(2 + group), "r"(threads) : "memory");
 }
-__device__ __forceinline__ void compute_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+template <class T>
+__device__ __forceinline__ void compute_barrier() {
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * T::kWarps) : "memory");
+}
 
 // What a block shares besides the rows of x, the ring and the partial sums.
 struct Shared {
@@ -191,18 +199,23 @@ struct Shared {
     int failed;                     // a wait gave up: all later waits return at once
 };
 
+__device__ __noinline__ void slow_wait(Shared &sh, uint32_t bar, uint32_t parity) {
+    volatile int *failed = &sh.failed;
+    if (!*failed && !ptx::mbar_wait(bar, parity)) *failed = 1;
+}
 __device__ __forceinline__ void wait_or_fail(Shared &sh, uint64_t &bar, uint32_t parity) {
-    if (*reinterpret_cast<volatile int *>(&sh.failed)) return;
-    if (!ptx::mbar_wait(ptx::smem_u32(&bar), parity)) *reinterpret_cast<volatile int *>(&sh.failed) = 1;
+    const uint32_t a = ptx::smem_u32(&bar);
+    if (!ptx::mbar_test_wait(a, parity)) slow_wait(sh, a, parity);
 }
 
 // Rows per expert and the first tile of each.  Called by the whole block.
+template <class T>
 __device__ __forceinline__ void count_tiles(const Params &q, Shared &sh) {
     const int tid = threadIdx.x;
-    for (int e = tid; e < q.E; e += kThreads) sh.count[e] = q.row_ids ? 0 : q.R;
+    for (int e = tid; e < q.E; e += T::kThreads) sh.count[e] = q.row_ids ? 0 : q.R;
     __syncthreads();
     if (q.row_ids) {
-        for (int r = tid; r < q.R; r += kThreads) {
+        for (int r = tid; r < q.R; r += T::kThreads) {
             const int e = __ldg(q.row_ids + r);
             if (e >= 0 && e < q.E)
                 atomicAdd(&sh.count[e], 1);
@@ -233,12 +246,12 @@ __device__ __forceinline__ void count_tiles(const Params &q, Shared &sh) {
 
 // The rows of tile `slot` of expert e (ascending r), and their x as f16 in shared memory.
 // Called by the computing warps.  Returns the number of rows.
-template <class X>
+template <class T, class X>
 __device__ __forceinline__ int stage_x(const Params &q, Shared &sh, uint8_t *xs, int e, int slot) {
     const int tid = threadIdx.x, lane = tid & 31;
     const int j0 = (slot - sh.start[e]) * q.L.nt;
     const int ntok = min(q.L.nt, sh.count[e] - j0);
-    compute_barrier();              // the previous tile's rows are no longer read
+    compute_barrier<T>();              // the previous tile's rows are no longer read
     if (tid < 32) {
         if (q.row_ids) {
             int seen = 0;
@@ -255,7 +268,7 @@ __device__ __forceinline__ int stage_x(const Params &q, Shared &sh, uint8_t *xs,
         }
         if (lane < kTok) sh.tok_max[lane] = 0u;
     }
-    compute_barrier();
+    compute_barrier<T>();
     const int words = q.K / 8;
     const auto row_of = [&](int t) {
         return reinterpret_cast<const uint4 *>(static_cast<const X *>(q.x) + (sh.tok_row[t] / q.rows_per_x) * q.x_stride);
@@ -264,7 +277,7 @@ __device__ __forceinline__ int stage_x(const Params &q, Shared &sh, uint8_t *xs,
         for (int t = 0; t < ntok; ++t) {
             const uint4 *src = row_of(t);
             unsigned m = 0;
-            for (int c = tid; c < words; c += 32 * kWarps) {
+            for (int c = tid; c < words; c += 32 * T::kWarps) {
                 const uint4 v = __ldg(src + c);
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -277,7 +290,7 @@ __device__ __forceinline__ int stage_x(const Params &q, Shared &sh, uint8_t *xs,
             m = __reduce_max_sync(0xFFFFFFFFu, m);
             if (lane == 0 && m) atomicMax(&sh.tok_max[t], m);
         }
-        compute_barrier();
+        compute_barrier<T>();
         for (int t = 0; t < ntok; ++t) {
             const uint4 *src = row_of(t);
             const unsigned m = sh.tok_max[t];
@@ -285,7 +298,7 @@ __device__ __forceinline__ int stage_x(const Params &q, Shared &sh, uint8_t *xs,
             const int ex = m ? max((int)(m >> 7) - 127 - 14, -120) : 0;
             const float f = __uint_as_float((uint32_t)(127 - ex) << 23);
             if (tid == 0) sh.tok_exp[t] = ex;
-            for (int c = tid; c < words; c += 32 * kWarps) {
+            for (int c = tid; c < words; c += 32 * T::kWarps) {
                 const uint4 v = __ldg(src + c);
                 uint4 h;
                 h.x = pack_f16x2(bf16lo_to_f32(v.x) * f, bf16hi_to_f32(v.x) * f);
@@ -299,11 +312,11 @@ __device__ __forceinline__ int stage_x(const Params &q, Shared &sh, uint8_t *xs,
         for (int t = 0; t < ntok; ++t) {
             const uint4 *src = row_of(t);
             if (tid == 0) sh.tok_exp[t] = 0;
-            for (int c = tid; c < words; c += 32 * kWarps)
+            for (int c = tid; c < words; c += 32 * T::kWarps)
                 *reinterpret_cast<uint4 *>(xs + t * q.L.xs + c * 16) = __ldg(src + c);
         }
     }
-    compute_barrier();
+    compute_barrier<T>();
     return ntok;
 }
 
@@ -330,11 +343,10 @@ __device__ __forceinline__ void issue_scales(const Params &q, uint8_t *dst, uint
 }
 
 // What a warp keeps of the rows of its group while it works on an item.  Lane l stands for
-// row l when the scales become factors.
+// row l when the scales become factors; lanes without a row of the matrix read its first.
 struct RowScales {
     uint32_t bytes;      // shared address of the row's scale bytes
-    bool valid;          // the row exists
-    bool bad;            // an invalid scale was met
+    uint32_t worst;      // MXFP4: the largest scale met; NVFP4: without the sign
     int ref;             // MXFP4: factors are relative to this scale
 };
 
@@ -349,30 +361,25 @@ __device__ __forceinline__ void make_factors(uint32_t factors, RowScales &rs, in
     const uint32_t dst = factors + (g * 2 * T::kTiles + r) * 4;
     constexpr int kStep = 8 * 2 * T::kTiles * 4;        // bytes of the factors of one block (half)
     if constexpr (kNv) {
-        uint32_t worst = 0;
 #pragma unroll
         for (int i = 0; i < kWarpBlocks; ++i) {
-            uint32_t c0 = 0, c1 = 0;
-            if (rs.valid && i < n) {
-                c0 = lds8(rs.bytes + 2 * (first + i));
-                c1 = lds8(rs.bytes + 2 * (first + i) + 1);
-            }
-            worst = max(worst, max(c0 & 0x7Fu, c1 & 0x7Fu));
-            const uint32_t both = e4m3x2_to_f16x2(c0 | (c1 << 8));
+            if (i >= n) break;
+            const uint32_t a = rs.bytes + 2 * (first + i), c = lds8(a) | (lds8(a + 1) << 8);
+            rs.worst = max(rs.worst, max(c & 0x7Fu, (c >> 8) & 0x7Fu));
+            const uint32_t both = e4m3x2_to_f16x2(c);
             if (mine) {
                 sts32(dst + 2 * i * kStep, __byte_perm(both, both, 0x1010));
                 sts32(dst + (2 * i + 1) * kStep, __byte_perm(both, both, 0x3232));
             }
         }
-        rs.bad |= worst == 0x7Fu;
     } else {
         int s[kWarpBlocks], top = 0;
 #pragma unroll
         for (int i = 0; i < kWarpBlocks; ++i) {
-            s[i] = rs.valid && i < n ? (int)lds8(rs.bytes + first + i) : 0;
+            s[i] = (int)lds8(rs.bytes + first + min(i, n - 1));
             top = max(top, s[i]);
         }
-        rs.bad |= top == 255;
+        rs.worst = max(rs.worst, (uint32_t)top);
         if (rs.ref < 0) rs.ref = top;
         // Factors stay below 2^64: when a later stage brings larger scales, the sums are
         // brought to the new reference.
@@ -389,8 +396,9 @@ __device__ __forceinline__ void make_factors(uint32_t factors, RowScales &rs, in
                 }
         }
         if (mine) {
+            const int low = rs.ref - 127;
 #pragma unroll
-            for (int i = 0; i < kWarpBlocks; ++i) sts32(dst + i * kStep, (uint32_t)max(s[i] - rs.ref + 127, 0) << 23);
+            for (int i = 0; i < kWarpBlocks; ++i) sts32(dst + i * kStep, (uint32_t)(max(s[i], low) - low) << 23);
         }
     }
     __syncwarp();
@@ -401,13 +409,13 @@ __device__ __forceinline__ void make_factors(uint32_t factors, RowScales &rs, in
 // is free as long as both operands use it).  Swizzled boxes: the 16-byte unit u of row r
 // lies at unit u ^ (r % 8), and a block is a unit.  acc: rows g, g + 8 of tile m x columns
 // 2t, 2t + 1.
-template <class T, bool kNv>
+template <class T, bool kNv, bool kWhole>
 __device__ __forceinline__ void multiply_blocks(uint32_t weights, uint32_t x, uint32_t factors, int unit, int n,
                                                 float (&acc)[T::kTiles][4]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int i = 0; i < kWarpBlocks; ++i) {
-        if (i >= n) break;
+        if (!kWhole && i >= n) break;
         const uint32_t w = weights + (((unit + i) ^ g) << 4);
         const uint4 xv = lds128(x + i * 64);
         uint32_t f[2 * T::kTiles];
@@ -447,7 +455,7 @@ __device__ __forceinline__ void multiply_blocks(uint32_t weights, uint32_t x, ui
 }
 
 template <class T, class X, class Out, bool kNv, bool kSwiGlu>
-__global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const __grid_constant__ CUtensorMap weights,
+__global__ void __launch_bounds__(T::kThreads, T::kBlocksPerSm) matvec_kernel(const __grid_constant__ CUtensorMap weights,
                                                              const __grid_constant__ Params q) {
     extern __shared__ uint8_t dynamic_smem[];
     __shared__ Shared sh;
@@ -456,18 +464,18 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const __grid_consta
     if (tid == 0) {
         for (int i = 0; i < q.L.stages; ++i) {
             ptx::mbar_init(ptx::smem_u32(&sh.full[i]), 1);
-            ptx::mbar_init(ptx::smem_u32(&sh.empty[i]), kWarps);
+            ptx::mbar_init(ptx::smem_u32(&sh.empty[i]), T::kWarps);
         }
         for (int i = 0; i < q.L.scale_bufs; ++i) {
             ptx::mbar_init(ptx::smem_u32(&sh.scales_full[i]), 1);
-            ptx::mbar_init(ptx::smem_u32(&sh.scales_empty[i]), kWarps);
+            ptx::mbar_init(ptx::smem_u32(&sh.scales_empty[i]), T::kWarps);
         }
         ptx::fence_mbarrier_init();
         sh.failed = 0;
     }
     pdl_wait();
     pdl_trigger();
-    count_tiles(q, sh);
+    count_tiles<T>(q, sh);
     const int n_tiles = (q.N + T::kRows - 1) / T::kRows, chunks = (q.K + T::kStageK - 1) / T::kStageK;
     const int64_t items = (int64_t)sh.start[q.E] * n_tiles;
     const int beg = (int)(items * blockIdx.x / gridDim.x), end = (int)(items * (blockIdx.x + 1) / gridDim.x);
@@ -475,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const __grid_consta
     int stage = 0, sbuf = 0;
     uint32_t phase = 0, sphase = 0;
 
-    if (warp == kWarps) {
+    if (warp == T::kWarps) {
         for (int it = beg; it < end; ++it) {
             while (sh.start[e + 1] <= slot) ++e;
             const int n0 = tile * T::kRows;
@@ -518,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const __grid_consta
     const int per_row = q.K / (kNv ? 16 : 32);
     const int n_out = kSwiGlu ? q.N / 2 : q.N;
     const uint32_t ring = ptx::smem_u32(sm) + part / 2 * T::kBoxBytes + (group * T::kGroupRows + g) * 128 + t * 4;
-    const uint32_t factors = ptx::smem_u32(sm + q.L.factors) + warp * (kNv ? 2 : 1) * (T::kFactorBytes / kWarps);
+    const uint32_t factors = ptx::smem_u32(sm + q.L.factors) + warp * (kNv ? 2 : 1) * (T::kFactorBytes / T::kWarps);
     float *red = reinterpret_cast<float *>(sm + q.L.red) + group * T::kSplit * T::kGroupRows * kTok;
     int staged = -1, ntok = 0;
     int tok_exp[2] = {0, 0};
@@ -527,20 +535,29 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const __grid_consta
         const int n0 = tile * T::kRows + group * T::kGroupRows;      // this group's first row
         if (slot != staged) {
             while (sh.start[e + 1] <= slot) ++e;
-            ntok = stage_x<X>(q, sh, sm + q.L.x, e, slot);
+            ntok = stage_x<T, X>(q, sh, sm + q.L.x, e, slot);
             staged = slot;
 #pragma unroll
             for (int i = 0; i < 2; ++i) tok_exp[i] = 2 * t + i < ntok ? sh.tok_exp[2 * t + i] : 0;
             // columns past the staged rows repeat the last one (and are not stored)
             x0 = ptx::smem_u32(sm + q.L.x) + min(g, ntok - 1) * q.L.xs + part * (kWarpBlocks * 64) + t * 16;
         }
+        const int my_row = lane < T::kGroupRows && n0 + lane < q.N ? group * T::kGroupRows + lane : 0;
         RowScales rs;
-        rs.valid = lane < T::kGroupRows && n0 + lane < q.N;
-        rs.bad = false;
+        rs.worst = 0;
         rs.ref = -1;
         rs.bytes = ptx::smem_u32(sm + q.L.scales) + sbuf * q.L.scale_bytes +
-                   ((uint32_t)(e * q.N + tile * T::kRows) * (uint32_t)per_row & 15u) +
-                   (group * T::kGroupRows + lane) * per_row;
+                   ((uint32_t)(e * q.N + tile * T::kRows) * (uint32_t)per_row & 15u) + my_row * per_row;
+        // the bias and scale of the outputs this thread will store
+        constexpr int kOut = T::kGroupRows * kTok / (32 * T::kSplit) > 0 ? T::kGroupRows * kTok / (32 * T::kSplit) : 1;
+        float bias[kOut], scale2[kOut];
+#pragma unroll
+        for (int j = 0; j < kOut; ++j) {
+            const int row = (part * 32 + lane + j * 32 * T::kSplit) / kTok, n = n0 + row;
+            const bool live = row < T::kGroupRows && n < q.N;
+            bias[j] = live && q.bias ? __ldg(q.bias + (int64_t)e * q.N + n) : 0.0f;
+            scale2[j] = kNv && live && q.scale2 ? __ldg(q.scale2 + (kSwiGlu ? 2 * e + (row & 1) : e)) : 1.0f;
+        }
         wait_or_fail(sh, sh.scales_full[sbuf], sphase);
         float acc[T::kTiles][4];
 #pragma unroll
@@ -549,9 +566,13 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const __grid_consta
             const int first = c * (T::kStageK / 32) + part * kWarpBlocks, n = min(kWarpBlocks, q.K / 32 - first);
             if (n > 0) make_factors<T, kNv>(factors, rs, first, n, acc);
             wait_or_fail(sh, sh.full[stage], phase);
-            if (n > 0)
-                multiply_blocks<T, kNv>(ring + stage * T::kStageBytes, x0 + c * (T::kStageK * 2), factors,
-                                        (part & 1) * kWarpBlocks, n, acc);
+            // whole stages without a test per block, so that all their loads go out first
+            if (n == kWarpBlocks)
+                multiply_blocks<T, kNv, true>(ring + stage * T::kStageBytes, x0 + c * (T::kStageK * 2), factors,
+                                              (part & 1) * kWarpBlocks, n, acc);
+            else if (n > 0)
+                multiply_blocks<T, kNv, false>(ring + stage * T::kStageBytes, x0 + c * (T::kStageK * 2), factors,
+                                               (part & 1) * kWarpBlocks, n, acc);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.empty[stage]));
             if (++stage == q.L.stages) {
@@ -564,17 +585,34 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const __grid_consta
             sbuf = 0;
             sphase ^= 1u;
         }
-        if (rs.bad && rs.valid) raise_device_error(MOE_DEVERR_BAD_SCALE);
+        if (rs.worst == (kNv ? 127u : 255u)) raise_device_error(MOE_DEVERR_BAD_SCALE);
         if constexpr (!kNv) {
-            // from the reference scales and the staged x to the true scale; a row with an invalid scale is NaN
-            const int row_e = rs.bad ? 1 << 20 : rs.ref - 127;
+            // from the reference scales and the staged x to the true scale
+            int ex[T::kTiles][2];
+            bool plain = rs.worst != 255u;
 #pragma unroll
             for (int m = 0; m < T::kTiles; ++m)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int re = __shfl_sync(0xFFFFFFFFu, row_e, g + 8 * (i >> 1) + 16 * m);
-                    acc[m][i] = re == 1 << 20 ? __uint_as_float(0x7FC00000u) : scale_pow2(acc[m][i], re + tok_exp[i & 1]);
+                for (int h = 0; h < 2; ++h) {
+                    ex[m][h] = __shfl_sync(0xFFFFFFFFu, rs.ref - 127, g + 8 * h + 16 * m);
+                    plain = plain && min(ex[m][h] + tok_exp[0], ex[m][h] + tok_exp[1]) >= -126 &&
+                            max(ex[m][h] + tok_exp[0], ex[m][h] + tok_exp[1]) <= 127;
                 }
+            if (__all_sync(0xFFFFFFFFu, plain)) {
+#pragma unroll
+                for (int m = 0; m < T::kTiles; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[m][i] *= __uint_as_float((uint32_t)(ex[m][i >> 1] + tok_exp[i & 1] + 127) << 23);
+            } else {              // exponents past fp32's own, or a row that an invalid scale makes NaN
+#pragma unroll
+                for (int m = 0; m < T::kTiles; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool bad = __shfl_sync(0xFFFFFFFFu, rs.worst, g + 8 * (i >> 1) + 16 * m) == 255u;
+                        acc[m][i] = bad ? __uint_as_float(0x7FC00000u) : scale_pow2(acc[m][i], ex[m][i >> 1] + tok_exp[i & 1]);
+                    }
+            }
         }
         // join the warps' sums
         group_barrier(group, 32 * T::kSplit);          // the previous item's are read
@@ -585,19 +623,17 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const __grid_consta
             *reinterpret_cast<float2 *>(mine + 8 * kTok) = make_float2(acc[m][2], acc[m][3]);
         }
         group_barrier(group, 32 * T::kSplit);
-        for (int o = part * 32 + lane; o < T::kGroupRows * kTok; o += 32 * T::kSplit) {
+#pragma unroll
+        for (int j = 0; j < kOut; ++j) {
+            const int o = part * 32 + lane + j * 32 * T::kSplit;
+            if (o >= T::kGroupRows * kTok) break;                      // whole warps
             const int row = o / kTok, tok = o % kTok, n = n0 + row;
             float v = 0.0f;
 #pragma unroll
             for (int w = 0; w < T::kSplit; ++w) v += red[w * T::kGroupRows * kTok + o];
             const bool live = n < q.N && tok < ntok;
-            if (live) {
-                if constexpr (kNv) {
-                    v = scale_pow2(v, sh.tok_exp[tok]);
-                    if (q.scale2) v *= __ldg(q.scale2 + (kSwiGlu ? 2 * e + (row & 1) : e));
-                }
-                if (q.bias) v += __ldg(q.bias + (int64_t)e * q.N + n);
-            }
+            if constexpr (kNv) v = live ? scale_pow2(v, sh.tok_exp[tok]) * scale2[j] : 0.0f;
+            v += bias[j];
             if constexpr (kSwiGlu) {
                 const float up = __shfl_xor_sync(0xFFFFFFFFu, v, kTok);      // row + 1
                 if (live && !(row & 1))

@@ -823,7 +823,7 @@ moe::mv::Layout matvec_layout(int64_t R, int64_t K, int block, int limit) {
     L.nt = (int)std::min<int64_t>(std::min<int64_t>(mv::kTok, R), fit);
     if (L.nt < 1) return L;
     const int x_bytes = (L.nt * L.xs + 127) / 128 * 128;
-    for (const int room : {limit / 2, limit}) {
+    for (const int room : {limit / T::kBlocksPerSm, limit}) {
         for (L.scale_bufs = 2; L.scale_bufs >= 1; --L.scale_bufs) {
             L.stages = std::min((room - fixed - x_bytes - L.scale_bufs * L.scale_bytes) / T::kStageBytes, mv::kMaxStages);
             if (L.stages >= 2) break;
@@ -865,11 +865,11 @@ int launch_matvec_tile(moe::mv::Params q, const uint8_t *blocks, int optin, cuda
     if (!make_matvec_map(&map, blocks, (int64_t)q.E * q.N, q.K, T::kRows)) return MOE_ERR_CUDA;
     auto kernel = mv::matvec_kernel<T, X, Out, kNv, kSwiGlu>;
     if (!ensure_smem_attr(reinterpret_cast<const void *>(kernel), q.L.total)) return MOE_ERR_CUDA;
-    const int per_sm = 2 * (q.L.total + (int)sizeof(mv::Shared) + 1024) <= optin + 1024 ? 2 : 1;
+    const int per_sm = T::kBlocksPerSm * (q.L.total + (int)sizeof(mv::Shared) + 1024) <= optin + 1024 ? T::kBlocksPerSm : 1;
     const int64_t grid = std::min<int64_t>(matvec_slots(q, q.L.nt) * moe::ceil_div(q.N, T::kRows),
                                            (int64_t)sm_count() * per_sm);
     StageScope scope(kSwiGlu ? MOE_STAGE_GATE_UP : MOE_STAGE_DOWN, s);
-    launch_pdl(kernel, dim3((unsigned)grid), dim3(mv::kThreads), q.L.total, s, map, q);
+    launch_pdl(kernel, dim3((unsigned)grid), dim3(T::kThreads), q.L.total, s, map, q);
     return launch_check();
 }
 
