@@ -43,38 +43,36 @@ namespace moe {
 namespace mv {
 
 constexpr int kTok = 8;                // rows of x of an item (mma N)
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 8;
 constexpr int kMaxExperts = 256;
-constexpr int kWarpBlocks = 4;         // 32-element blocks of a warp in one stage
+constexpr int kMaxRows = 1024;
 
 // kWarps computing warps (one more issues the copies), kSplit of them over the K of each
-// group of 16 * kTiles weight rows; kBlocksPerSm such blocks on an SM.
-template <int kWarps_, int kSplit_, int kTiles_, int kBlocksPerSm_>
+// group of 16 * kTiles weight rows, with kBlocks 32-element blocks of every stage each.
+template <int kWarps_, int kSplit_, int kTiles_, int kBlocks_>
 struct Tile {
-    static constexpr int kWarps = kWarps_, kSplit = kSplit_, kTiles = kTiles_, kBlocksPerSm = kBlocksPerSm_;
+    static constexpr int kWarps = kWarps_, kSplit = kSplit_, kTiles = kTiles_, kBlocks = kBlocks_;
     static constexpr int kThreads = 32 * (kWarps + 1);
     static constexpr int kGroups = kWarps / kSplit;
     static constexpr int kGroupRows = 16 * kTiles;
     static constexpr int kRows = kGroups * kGroupRows;           // weight rows of an item
-    static constexpr int kStageK = kSplit * kWarpBlocks * 32;    // their elements in a stage
+    static constexpr int kStageK = kSplit * kBlocks * 32;        // their elements in a stage
     static constexpr int kBoxBytes = kRows * 128;                // 256 elements of every row
     static constexpr int kStageBytes = kStageK / 256 * kBoxBytes;
     static constexpr int kRedBytes = kWarps * kGroupRows * kTok * 4;
-    static constexpr int kFactorBytes = kWarps * kWarpBlocks * kGroupRows * 4;   // twice that for NVFP4
+    static constexpr int kFactorBytes = kWarps * kBlocks * kGroupRows * 4;   // twice that for NVFP4
+    static_assert(kStageK % 256 == 0 && kTiles == 2, "whole boxes; a lane per row of the group");
 };
-#ifndef MOE_WIDE
-#define MOE_WIDE 16, 4, 2, 1
-#endif
-using WideTile = Tile<MOE_WIDE>;        // 128 rows x 512 elements a stage
-using NarrowTile = Tile<8, 8, 1, 2>;    // 16 rows x 1024 elements a stage
 
 // Shared-memory layout of a call (host-computed; offsets and strides in bytes from a
 // 1024-byte boundary).
 struct Layout {
     int nt;                // rows of x per tile, at most kTok
+    int rows;              // weight rows of an item
     int stages;            // of the weight ring, which starts at 0
     int scale_bufs;        // items whose scales are held
-    int scale_bytes;       // of one item
+    int scale_stride;      // of a weight row's scales
+    int scale_bytes;       // of one item's scales, and its bias (fp32) and scale2 behind them
     int xs;                // stride of a row of x
     int x, scales, red, factors, total;
 };
@@ -146,21 +144,20 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Loads of shared memory in program order with the barriers around them, but free to move
-// past arithmetic.
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+// Loads of shared memory keep their order with the barriers around them, but may move past
+// arithmetic.
+// Four 8-row x 16-byte matrices, a row address from each lane (lane l: row l % 8 of matrix
+// l / 8): lane (g, t) receives word t of row g of each.
+__device__ __forceinline__ uint4 ldmatrix4(uint32_t a) {
+    uint4 v;
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a));
     return v;
 }
 __device__ __forceinline__ uint32_t lds8(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
     return v;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -178,7 +175,6 @@ __device__ __forceinline__ float scale_pow2(float v, int e) {
 __device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
     asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
-
 __device__ __forceinline__ void group_barrier(int group, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(2 + group), "r"(threads) : "memory");
 }
@@ -191,12 +187,14 @@ __device__ __forceinline__ void compute_barrier() {
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages];      // weight stages
     uint64_t scales_full[2], scales_empty[2];
+    uint64_t red_empty[8];          // a group's partial sums are read
     int count[kMaxExperts];         // rows per expert
     int start[kMaxExperts + 1];     // first tile of each expert
     int tok_row[kTok];              // rows r of the staged tile
     int tok_exp[kTok];              // x = staged value * 2^tok_exp
     unsigned tok_max[kTok];
     int failed;                     // a wait gave up: all later waits return at once
+    int16_t ids[kMaxRows];          // the rows' experts, -1 outside [0, E)
 };
 
 __device__ __noinline__ void slow_wait(Shared &sh, uint32_t bar, uint32_t parity) {
@@ -217,7 +215,9 @@ __device__ __forceinline__ void count_tiles(const Params &q, Shared &sh) {
     if (q.row_ids) {
         for (int r = tid; r < q.R; r += T::kThreads) {
             const int e = __ldg(q.row_ids + r);
-            if (e >= 0 && e < q.E)
+            const bool known = e >= 0 && e < q.E;
+            sh.ids[r] = known ? (int16_t)e : (int16_t)-1;
+            if (known)
                 atomicAdd(&sh.count[e], 1);
             else if (blockIdx.x == 0)
                 raise_device_error(MOE_DEVERR_BAD_EXPERT_ID);
@@ -244,99 +244,125 @@ __device__ __forceinline__ void count_tiles(const Params &q, Shared &sh) {
     __syncthreads();
 }
 
+// Rows of tile `slot` of expert e.
+__device__ __forceinline__ int tile_rows(const Params &q, const Shared &sh, int e, int slot) {
+    return min(q.L.nt, sh.count[e] - (slot - sh.start[e]) * q.L.nt);
+}
+
 // The rows of tile `slot` of expert e (ascending r), and their x as f16 in shared memory.
-// Called by the computing warps.  Returns the number of rows.
+// Called by the computing warps.  Returns the number of rows.  This sits on the critical
+// path of a small call and of each change of expert, so it crosses global memory once,
+// with all warps on all rows at once (a unit of work is 128 16-byte words of a row, four
+// loads in flight a lane); bf16 is converted in place once the rows' largest values are known.
 template <class T, class X>
 __device__ __forceinline__ int stage_x(const Params &q, Shared &sh, uint8_t *xs, int e, int slot) {
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int j0 = (slot - sh.start[e]) * q.L.nt;
-    const int ntok = min(q.L.nt, sh.count[e] - j0);
-    compute_barrier<T>();              // the previous tile's rows are no longer read
-    if (tid < 32) {
+    const int ntok = tile_rows(q, sh, e, slot);
+    int *tok_row = sh.tok_row, *tok_exp = sh.tok_exp;
+    compute_barrier<T>();           // the previous tile's rows are no longer read
+    if (warp == 0) {
         if (q.row_ids) {
-            int seen = 0;
-            for (int base = 0; base < q.R && seen < j0 + ntok; base += 32) {
+            for (int base = 0, seen = 0; base < q.R && seen < j0 + ntok; base += 32) {
                 const int r = base + lane;
-                const bool mine = r < q.R && __ldg(q.row_ids + r) == e;
+                const bool mine = r < q.R && sh.ids[r] == e;
                 const unsigned m = __ballot_sync(0xFFFFFFFFu, mine);
                 const int rank = seen + __popc(m & ((1u << lane) - 1u)) - j0;
-                if (mine && rank >= 0 && rank < ntok) sh.tok_row[rank] = r;
+                if (mine && rank >= 0 && rank < ntok) tok_row[rank] = r;
                 seen += __popc(m);
             }
         } else if (lane < ntok) {
-            sh.tok_row[lane] = j0 + lane;
+            tok_row[lane] = j0 + lane;
         }
         if (lane < kTok) sh.tok_max[lane] = 0u;
     }
     compute_barrier<T>();
-    const int words = q.K / 8;
-    const auto row_of = [&](int t) {
-        return reinterpret_cast<const uint4 *>(static_cast<const X *>(q.x) + (sh.tok_row[t] / q.rows_per_x) * q.x_stride);
-    };
-    if constexpr (std::is_same<X, __nv_bfloat16>::value) {
-        for (int t = 0; t < ntok; ++t) {
-            const uint4 *src = row_of(t);
-            unsigned m = 0;
-            for (int c = tid; c < words; c += 32 * T::kWarps) {
-                const uint4 v = __ldg(src + c);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    constexpr bool kScaled = std::is_same<X, __nv_bfloat16>::value;
+    const int words = q.K / 8, segs = (words + 127) / 128;
+    for (int u = warp; u < ntok * segs; u += T::kWarps) {
+        const int t = u / segs, c0 = (u - t * segs) * 128 + lane;
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const X *>(q.x) +
+                                                           (tok_row[t] / q.rows_per_x) * q.x_stride);
+        uint4 v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const unsigned lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
-                    if (lo < 0x7F80u) m = max(m, lo);
-                    if (hi < 0x7F80u) m = max(m, hi);
+        for (int i = 0; i < 4; ++i) v[i] = c0 + 32 * i < words ? __ldg(src + c0 + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+        unsigned m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (c0 + 32 * i < words) *reinterpret_cast<uint4 *>(xs + t * q.L.xs + (c0 + 32 * i) * 16) = v[i];
+            if constexpr (kScaled) {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const unsigned lo = w[j] & 0x7FFFu, hi = (w[j] >> 16) & 0x7FFFu;
+                    m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
                 }
             }
+        }
+        if constexpr (kScaled) {
             m = __reduce_max_sync(0xFFFFFFFFu, m);
             if (lane == 0 && m) atomicMax(&sh.tok_max[t], m);
         }
+    }
+    if constexpr (kScaled) {
         compute_barrier<T>();
-        for (int t = 0; t < ntok; ++t) {
-            const uint4 *src = row_of(t);
+        for (int u = warp; u < ntok * segs; u += T::kWarps) {
+            const int t = u / segs, c0 = (u - t * segs) * 128 + lane;
             const unsigned m = sh.tok_max[t];
             // exponent of the largest value, less 14; at least -120, so that 2^-exp is a normal fp32
             const int ex = m ? max((int)(m >> 7) - 127 - 14, -120) : 0;
             const float f = __uint_as_float((uint32_t)(127 - ex) << 23);
-            if (tid == 0) sh.tok_exp[t] = ex;
-            for (int c = tid; c < words; c += 32 * T::kWarps) {
-                const uint4 v = __ldg(src + c);
-                uint4 h;
-                h.x = pack_f16x2(bf16lo_to_f32(v.x) * f, bf16hi_to_f32(v.x) * f);
-                h.y = pack_f16x2(bf16lo_to_f32(v.y) * f, bf16hi_to_f32(v.y) * f);
-                h.z = pack_f16x2(bf16lo_to_f32(v.z) * f, bf16hi_to_f32(v.z) * f);
-                h.w = pack_f16x2(bf16lo_to_f32(v.w) * f, bf16hi_to_f32(v.w) * f);
-                *reinterpret_cast<uint4 *>(xs + t * q.L.xs + c * 16) = h;
+            if (c0 == 0) tok_exp[t] = ex;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (c0 + 32 * i >= words) continue;
+                uint4 *p = reinterpret_cast<uint4 *>(xs + t * q.L.xs + (c0 + 32 * i) * 16);
+                const uint4 v = *p;
+                *p = make_uint4(pack_f16x2(bf16lo_to_f32(v.x) * f, bf16hi_to_f32(v.x) * f),
+                                pack_f16x2(bf16lo_to_f32(v.y) * f, bf16hi_to_f32(v.y) * f),
+                                pack_f16x2(bf16lo_to_f32(v.z) * f, bf16hi_to_f32(v.z) * f),
+                                pack_f16x2(bf16lo_to_f32(v.w) * f, bf16hi_to_f32(v.w) * f));
             }
         }
-    } else {
-        for (int t = 0; t < ntok; ++t) {
-            const uint4 *src = row_of(t);
-            if (tid == 0) sh.tok_exp[t] = 0;
-            for (int c = tid; c < words; c += 32 * T::kWarps)
-                *reinterpret_cast<uint4 *>(xs + t * q.L.xs + c * 16) = __ldg(src + c);
-        }
+    } else if (tid < ntok) {
+        tok_exp[tid] = 0;
     }
     compute_barrier<T>();
     return ntok;
 }
 
-// The scale bytes of weight rows n0 .. n0 + rows - 1 of expert e: a run of bytes that starts
-// anywhere, copied as the 16-byte granules that hold it (the first byte lands at its
-// address modulo 16).  Called by one warp; arrives once on `full`.
-template <bool kNv>
+// What an item needs besides codes: the scale bytes of weight rows n0 .. n0 + rows - 1 of
+// expert e, their bias (fp32, 0 without one) and scale2 (gate, up) behind them.  The scales
+// are a run of bytes that starts anywhere, copied as the 16-byte granules that hold it (the
+// first byte lands at its address modulo 16); where rows of a multiple of 32 bytes would
+// put the same bytes of many rows into one bank, a copy per row spreads them.  Called by
+// one warp; arrives once on `full`.
+template <bool kNv, bool kSwiGlu>
 __device__ __forceinline__ void issue_scales(const Params &q, uint8_t *dst, uint64_t &full, int e, int n0, int rows) {
     const int per_row = q.K / (kNv ? 16 : 32), lane = threadIdx.x & 31;
-    const int64_t first = ((int64_t)e * q.N + n0) * per_row, last = first + (int64_t)rows * per_row;
+    const uint32_t bar = ptx::smem_u32(&full);
+    const int64_t row0 = (int64_t)e * q.N + n0, first = row0 * per_row, last = first + (int64_t)rows * per_row;
+    float *tail = reinterpret_cast<float *>(dst + q.L.scale_bytes) - 2;
+    if (q.bias)
+        for (int r = lane; r < rows; r += 32) tail[r - q.L.rows] = __ldg(q.bias + row0 + r);
+    if (kNv && lane < 2) tail[lane] = q.scale2 ? __ldg(q.scale2 + (kSwiGlu ? 2 * e + lane : e)) : 1.0f;
+    if (q.L.scale_stride != per_row) {
+        if (lane == 0) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(rows * per_row));
+        __syncwarp();
+        for (int r = lane; r < rows; r += 32)
+            ptx::bulk_load(ptx::smem_u32(dst + r * q.L.scale_stride), q.scales + first + (int64_t)r * per_row, per_row, bar);
+        return;
+    }
     const int64_t total = (int64_t)q.E * q.N * per_row, lo = first & ~int64_t(15);
     int64_t hi = (last + 15) & ~int64_t(15);
     if (hi > total) {               // the bank's last bytes do not fill a granule: plain loads
         hi = total & ~int64_t(15);
         const int64_t i = max(hi, first) + lane;
         if (i < total) dst[i - lo] = __ldg(q.scales + i);
-        __syncwarp();
     }
+    __syncwarp();
     if (lane == 0) {
-        const uint32_t bar = ptx::smem_u32(&full), bytes = hi > lo ? (uint32_t)(hi - lo) : 0u;
+        const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) : 0u;
         ptx::mbar_arrive_expect_tx(bar, bytes);
         if (bytes) ptx::bulk_load(ptx::smem_u32(dst), q.scales + lo, bytes, bar);
     }
@@ -350,33 +376,29 @@ struct RowScales {
     int ref;             // MXFP4: factors are relative to this scale
 };
 
-// The factors of this warp's blocks first .. first + n - 1 (of 32 elements) of every row:
-// MXFP4 [block][g][row / 8] fp32, NVFP4 [block][half][g][row / 8] f16x2 (both halves the
-// scale), g = row % 8.
+// The factors of this warp's n blocks of a stage (block i of the warp is the stage's block
+// kSplit * i + part; `first` is block 0 counted from the row's start) for every row of the
+// group: MXFP4 [block][g][row / 8] fp32, NVFP4 [block][half][g][row / 8] f16x2 (both halves
+// the scale), g = row % 8.
 template <class T, bool kNv>
 __device__ __forceinline__ void make_factors(uint32_t factors, RowScales &rs, int first, int n,
                                              float (&acc)[T::kTiles][4]) {
-    const int lane = threadIdx.x & 31, g = lane & 7, r = lane >> 3;
-    const bool mine = lane < T::kGroupRows;
-    const uint32_t dst = factors + (g * 2 * T::kTiles + r) * 4;
-    constexpr int kStep = 8 * 2 * T::kTiles * 4;        // bytes of the factors of one block (half)
+    const int lane = threadIdx.x & 31;
+    const uint32_t dst = factors + ((lane & 7) * 4 + (lane >> 3)) * 4;
     if constexpr (kNv) {
 #pragma unroll
-        for (int i = 0; i < kWarpBlocks; ++i) {
-            if (i >= n) break;
-            const uint32_t a = rs.bytes + 2 * (first + i), c = lds8(a) | (lds8(a + 1) << 8);
+        for (int i = 0; i < T::kBlocks; ++i) {
+            const uint32_t a = rs.bytes + 2 * (first + T::kSplit * min(i, n - 1)), c = lds8(a) | (lds8(a + 1) << 8);
             rs.worst = max(rs.worst, max(c & 0x7Fu, (c >> 8) & 0x7Fu));
             const uint32_t both = e4m3x2_to_f16x2(c);
-            if (mine) {
-                sts32(dst + 2 * i * kStep, __byte_perm(both, both, 0x1010));
-                sts32(dst + (2 * i + 1) * kStep, __byte_perm(both, both, 0x3232));
-            }
+            sts32(dst + 2 * i * 128, __byte_perm(both, both, 0x1010));
+            sts32(dst + (2 * i + 1) * 128, __byte_perm(both, both, 0x3232));
         }
     } else {
-        int s[kWarpBlocks], top = 0;
+        int s[T::kBlocks], top = 0;
 #pragma unroll
-        for (int i = 0; i < kWarpBlocks; ++i) {
-            s[i] = (int)lds8(rs.bytes + first + min(i, n - 1));
+        for (int i = 0; i < T::kBlocks; ++i) {
+            s[i] = (int)lds8(rs.bytes + first + T::kSplit * min(i, n - 1));
             top = max(top, s[i]);
         }
         rs.worst = max(rs.worst, (uint32_t)top);
@@ -395,48 +417,40 @@ __device__ __forceinline__ void make_factors(uint32_t factors, RowScales &rs, in
                     acc[m][2 * h + 1] = scale_pow2(acc[m][2 * h + 1], -by);
                 }
         }
-        if (mine) {
-            const int low = rs.ref - 127;
+        const int low = rs.ref - 127;
 #pragma unroll
-            for (int i = 0; i < kWarpBlocks; ++i) sts32(dst + i * kStep, (uint32_t)(max(s[i], low) - low) << 23);
-        }
+        for (int i = 0; i < T::kBlocks; ++i) sts32(dst + i * 128, (uint32_t)(max(s[i], low) - low) << 23);
     }
     __syncwarp();
 }
 
-// This warp's n (at most kWarpBlocks) blocks of one stage.  Lane (g, t): rows g, g + 8, ...
-// of the group, row g of x, elements 8t .. 8t + 7 of a block (the order of k inside an mma
-// is free as long as both operands use it).  Swizzled boxes: the 16-byte unit u of row r
-// lies at unit u ^ (r % 8), and a block is a unit.  acc: rows g, g + 8 of tile m x columns
-// 2t, 2t + 1.
+// This warp's n blocks of one stage.  Lane (g, t): rows g, g + 8, g + 16, g + 24 of the
+// group, row g of x, elements 8t .. 8t + 7 of a block (the order of k inside an mma is free
+// as long as both operands use it).  Swizzled boxes: the 16-byte unit u of row r lies at
+// unit u ^ (r % 8), and a block is a unit.  `weights`: this lane's row for ldmatrix, in the
+// box of the warp's first block; `unit`: that block's place in the row.  acc: rows g, g + 8
+// of tile m x columns 2t, 2t + 1.  kWhole: n = kBlocks, without a test per block.
 template <class T, bool kNv, bool kWhole>
-__device__ __forceinline__ void multiply_blocks(uint32_t weights, uint32_t x, uint32_t factors, int unit, int n,
+__device__ __forceinline__ void multiply_blocks(uint32_t weights, uint32_t unit, uint32_t x, uint32_t factors, int n,
                                                 float (&acc)[T::kTiles][4]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int i = 0; i < kWarpBlocks; ++i) {
+    for (int i = 0; i < T::kBlocks; ++i) {
         if (!kWhole && i >= n) break;
-        const uint32_t w = weights + (((unit + i) ^ g) << 4);
-        const uint4 xv = lds128(x + i * 64);
-        uint32_t f[2 * T::kTiles];
-        const uint32_t fa = factors + (kNv ? (2 * i + (t >> 1)) * 8 + g : i * 8 + g) * 8 * T::kTiles;
-        if constexpr (T::kTiles == 2) {
-            const uint4 v = lds128(fa);
-            f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
-        } else {
-            const uint2 v = lds64(fa);
-            f[0] = v.x, f[1] = v.y;
-        }
+        const uint4 w = ldmatrix4(weights + T::kSplit * i / 8 * T::kBoxBytes + (unit ^ ((T::kSplit * i & 7) << 4)));
+        const uint4 xv = lds128(x + T::kSplit * i * 64);
+        const uint4 f = lds128(factors + (kNv ? (2 * i + (t >> 1)) * 128 : i * 128) + g * 16);
+        const uint32_t words[4] = {w.x, w.y, w.z, w.w}, factor[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
         for (int m = 0; m < T::kTiles; ++m) {
             uint32_t h0[4], h1[4];
-            e2m1x8_to_f16(lds32(w + m * 2048), h0);
-            e2m1x8_to_f16(lds32(w + m * 2048 + 1024), h1);
+            e2m1x8_to_f16(words[2 * m], h0);
+            e2m1x8_to_f16(words[2 * m + 1], h1);
             if constexpr (kNv) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    h0[j] = mul_f16x2(h0[j], f[2 * m]);
-                    h1[j] = mul_f16x2(h1[j], f[2 * m + 1]);
+                    h0[j] = mul_f16x2(h0[j], factor[2 * m]);
+                    h1[j] = mul_f16x2(h1[j], factor[2 * m + 1]);
                 }
                 mma_f16<false>(acc[m], h0[0], h1[0], h0[1], h1[1], xv.x, xv.y);
                 mma_f16<false>(acc[m], h0[2], h1[2], h0[3], h1[3], xv.z, xv.w);
@@ -444,7 +458,7 @@ __device__ __forceinline__ void multiply_blocks(uint32_t weights, uint32_t x, ui
                 float c[4];
                 mma_f16<true>(c, h0[0], h1[0], h0[1], h1[1], xv.x, xv.y);
                 mma_f16<false>(c, h0[2], h1[2], h0[3], h1[3], xv.z, xv.w);
-                const float f0 = __uint_as_float(f[2 * m]), f1 = __uint_as_float(f[2 * m + 1]);
+                const float f0 = __uint_as_float(factor[2 * m]), f1 = __uint_as_float(factor[2 * m + 1]);
                 acc[m][0] = fmaf(c[0], f0, acc[m][0]);
                 acc[m][1] = fmaf(c[1], f0, acc[m][1]);
                 acc[m][2] = fmaf(c[2], f1, acc[m][2]);
@@ -455,7 +469,7 @@ __device__ __forceinline__ void multiply_blocks(uint32_t weights, uint32_t x, ui
 }
 
 template <class T, class X, class Out, bool kNv, bool kSwiGlu>
-__global__ void __launch_bounds__(T::kThreads, T::kBlocksPerSm) matvec_kernel(const __grid_constant__ CUtensorMap weights,
+__global__ void __launch_bounds__(T::kThreads, 1) matvec_kernel(const __grid_constant__ CUtensorMap weights,
                                                              const __grid_constant__ Params q) {
     extern __shared__ uint8_t dynamic_smem[];
     __shared__ Shared sh;
@@ -470,6 +484,7 @@ __global__ void __launch_bounds__(T::kThreads, T::kBlocksPerSm) matvec_kernel(co
             ptx::mbar_init(ptx::smem_u32(&sh.scales_full[i]), 1);
             ptx::mbar_init(ptx::smem_u32(&sh.scales_empty[i]), T::kWarps);
         }
+        for (int i = 0; i < T::kGroups; ++i) ptx::mbar_init(ptx::smem_u32(&sh.red_empty[i]), T::kSplit);
         ptx::fence_mbarrier_init();
         sh.failed = 0;
     }
@@ -502,7 +517,7 @@ __global__ void __launch_bounds__(T::kThreads, T::kBlocksPerSm) matvec_kernel(co
                 if (c == 0) {
                     wait_or_fail(sh, sh.scales_empty[sbuf], sphase ^ 1u);
                     __syncwarp();
-                    issue_scales<kNv>(q, sm + q.L.scales + sbuf * q.L.scale_bytes, sh.scales_full[sbuf], e, n0,
+                    issue_scales<kNv, kSwiGlu>(q, sm + q.L.scales + sbuf * q.L.scale_bytes, sh.scales_full[sbuf], e, n0,
                                       min(T::kRows, q.N - n0));
                     if (++sbuf == q.L.scale_bufs) {
                         sbuf = 0;
@@ -522,12 +537,13 @@ __global__ void __launch_bounds__(T::kThreads, T::kBlocksPerSm) matvec_kernel(co
         return;
     }
 
+    constexpr int kRed = T::kGroupRows * kTok;         // outputs of a group
+    const int n_out = kSwiGlu ? q.N / 2 : q.N;
     const int group = warp / T::kSplit, part = warp % T::kSplit, g = lane >> 2, t = lane & 3;
     const int per_row = q.K / (kNv ? 16 : 32);
-    const int n_out = kSwiGlu ? q.N / 2 : q.N;
-    const uint32_t ring = ptx::smem_u32(sm) + part / 2 * T::kBoxBytes + (group * T::kGroupRows + g) * 128 + t * 4;
+    const uint32_t ring = ptx::smem_u32(sm) + part / 8 * T::kBoxBytes + (group * T::kGroupRows + lane) * 128;
+    const uint32_t unit = ((part ^ lane) & 7) << 4;
     const uint32_t factors = ptx::smem_u32(sm + q.L.factors) + warp * (kNv ? 2 : 1) * (T::kFactorBytes / T::kWarps);
-    float *red = reinterpret_cast<float *>(sm + q.L.red) + group * T::kSplit * T::kGroupRows * kTok;
     int staged = -1, ntok = 0;
     int tok_exp[2] = {0, 0};
     uint32_t x0 = 0;
@@ -540,50 +556,34 @@ __global__ void __launch_bounds__(T::kThreads, T::kBlocksPerSm) matvec_kernel(co
 #pragma unroll
             for (int i = 0; i < 2; ++i) tok_exp[i] = 2 * t + i < ntok ? sh.tok_exp[2 * t + i] : 0;
             // columns past the staged rows repeat the last one (and are not stored)
-            x0 = ptx::smem_u32(sm + q.L.x) + min(g, ntok - 1) * q.L.xs + part * (kWarpBlocks * 64) + t * 16;
+            x0 = ptx::smem_u32(sm + q.L.x) + min(g, ntok - 1) * q.L.xs + part * 64 + t * 16;
         }
-        const int my_row = lane < T::kGroupRows && n0 + lane < q.N ? group * T::kGroupRows + lane : 0;
+        const int my_row = n0 + lane < q.N ? group * T::kGroupRows + lane : 0;
         RowScales rs;
         rs.worst = 0;
         rs.ref = -1;
         rs.bytes = ptx::smem_u32(sm + q.L.scales) + sbuf * q.L.scale_bytes +
-                   ((uint32_t)(e * q.N + tile * T::kRows) * (uint32_t)per_row & 15u) + my_row * per_row;
-        // the bias and scale of the outputs this thread will store
-        constexpr int kOut = T::kGroupRows * kTok / (32 * T::kSplit) > 0 ? T::kGroupRows * kTok / (32 * T::kSplit) : 1;
-        float bias[kOut], scale2[kOut];
-#pragma unroll
-        for (int j = 0; j < kOut; ++j) {
-            const int row = (part * 32 + lane + j * 32 * T::kSplit) / kTok, n = n0 + row;
-            const bool live = row < T::kGroupRows && n < q.N;
-            bias[j] = live && q.bias ? __ldg(q.bias + (int64_t)e * q.N + n) : 0.0f;
-            scale2[j] = kNv && live && q.scale2 ? __ldg(q.scale2 + (kSwiGlu ? 2 * e + (row & 1) : e)) : 1.0f;
-        }
+                   ((uint32_t)(e * q.N + tile * T::kRows) * (uint32_t)per_row & 15u) + my_row * q.L.scale_stride;
         wait_or_fail(sh, sh.scales_full[sbuf], sphase);
         float acc[T::kTiles][4];
 #pragma unroll
         for (int m = 0; m < T::kTiles; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.0f;
         for (int c = 0; c < chunks; ++c) {
-            const int first = c * (T::kStageK / 32) + part * kWarpBlocks, n = min(kWarpBlocks, q.K / 32 - first);
+            const int first = c * (T::kStageK / 32) + part;
+            const int n = (q.K / 32 - first + T::kSplit - 1) / T::kSplit;        // at least kBlocks in a whole stage
             if (n > 0) make_factors<T, kNv>(factors, rs, first, n, acc);
             wait_or_fail(sh, sh.full[stage], phase);
-            // whole stages without a test per block, so that all their loads go out first
-            if (n == kWarpBlocks)
-                multiply_blocks<T, kNv, true>(ring + stage * T::kStageBytes, x0 + c * (T::kStageK * 2), factors,
-                                              (part & 1) * kWarpBlocks, n, acc);
+            const uint32_t w = ring + stage * T::kStageBytes, x = x0 + c * (T::kStageK * 2);
+            if (n >= T::kBlocks)
+                multiply_blocks<T, kNv, true>(w, unit, x, factors, n, acc);
             else if (n > 0)
-                multiply_blocks<T, kNv, false>(ring + stage * T::kStageBytes, x0 + c * (T::kStageK * 2), factors,
-                                               (part & 1) * kWarpBlocks, n, acc);
+                multiply_blocks<T, kNv, false>(w, unit, x, factors, n, acc);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.empty[stage]));
             if (++stage == q.L.stages) {
                 stage = 0;
                 phase ^= 1u;
             }
-        }
-        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.scales_empty[sbuf]));
-        if (++sbuf == q.L.scale_bufs) {
-            sbuf = 0;
-            sphase ^= 1u;
         }
         if (rs.worst == (kNv ? 127u : 255u)) raise_device_error(MOE_DEVERR_BAD_SCALE);
         if constexpr (!kNv) {
@@ -614,26 +614,28 @@ __global__ void __launch_bounds__(T::kThreads, T::kBlocksPerSm) matvec_kernel(co
                     }
             }
         }
-        // join the warps' sums
-        group_barrier(group, 32 * T::kSplit);          // the previous item's are read
+        // join the warps' sums, in warp order; then scale2, bias, activation, one rounding
+        float *red = reinterpret_cast<float *>(sm + q.L.red) + group * T::kSplit * kRed;
+        float *mine = red + part * kRed + g * kTok + 2 * t;
+        wait_or_fail(sh, sh.red_empty[group], ((it - beg) & 1) ^ 1u);      // the previous item's are read
 #pragma unroll
         for (int m = 0; m < T::kTiles; ++m) {
-            float *mine = red + (part * T::kGroupRows + 16 * m + g) * kTok + 2 * t;
-            *reinterpret_cast<float2 *>(mine) = make_float2(acc[m][0], acc[m][1]);
-            *reinterpret_cast<float2 *>(mine + 8 * kTok) = make_float2(acc[m][2], acc[m][3]);
+            *reinterpret_cast<float2 *>(mine + 16 * m * kTok) = make_float2(acc[m][0], acc[m][1]);
+            *reinterpret_cast<float2 *>(mine + (16 * m + 8) * kTok) = make_float2(acc[m][2], acc[m][3]);
         }
         group_barrier(group, 32 * T::kSplit);
+        const float *tail = reinterpret_cast<const float *>(sm + q.L.scales + (sbuf + 1) * q.L.scale_bytes) - 2;
 #pragma unroll
-        for (int j = 0; j < kOut; ++j) {
-            const int o = part * 32 + lane + j * 32 * T::kSplit;
-            if (o >= T::kGroupRows * kTok) break;                      // whole warps
-            const int row = o / kTok, tok = o % kTok, n = n0 + row;
+        for (int j = 0; j < (kRed + 32 * T::kSplit - 1) / (32 * T::kSplit); ++j) {
+            const int o = (j * T::kSplit + part) * 32 + lane;
+            if (o >= kRed) break;                                      // whole warps
+            const int row = group * T::kGroupRows + o / kTok, tok = o % kTok, n = tile * T::kRows + row;
             float v = 0.0f;
 #pragma unroll
-            for (int w = 0; w < T::kSplit; ++w) v += red[w * T::kGroupRows * kTok + o];
+            for (int w = 0; w < T::kSplit; ++w) v += red[w * kRed + o];
             const bool live = n < q.N && tok < ntok;
-            if constexpr (kNv) v = live ? scale_pow2(v, sh.tok_exp[tok]) * scale2[j] : 0.0f;
-            v += bias[j];
+            if constexpr (kNv) v = live ? scale_pow2(v, sh.tok_exp[tok]) * tail[kSwiGlu ? row & 1 : 0] : 0.0f;
+            if (q.bias) v += tail[row - T::kRows];
             if constexpr (kSwiGlu) {
                 const float up = __shfl_xor_sync(0xFFFFFFFFu, v, kTok);      // row + 1
                 if (live && !(row & 1))
@@ -642,6 +644,15 @@ __global__ void __launch_bounds__(T::kThreads, T::kBlocksPerSm) matvec_kernel(co
             } else if (live) {
                 static_cast<Out *>(q.out)[(int64_t)sh.tok_row[tok] * n_out + n] = f32_to_elem<Out>(v);
             }
+        }
+        __syncwarp();
+        if (lane == 0) {
+            ptx::mbar_arrive(ptx::smem_u32(&sh.red_empty[group]));
+            ptx::mbar_arrive(ptx::smem_u32(&sh.scales_empty[sbuf]));
+        }
+        if (++sbuf == q.L.scale_bufs) {
+            sbuf = 0;
+            sphase ^= 1u;
         }
         if (++tile == n_tiles) {
             tile = 0;

@@ -807,29 +807,30 @@ int sum_rows(const void *rows, int rows_dtype, int64_t rows_stride, int64_t T, i
 }
 
 // ---- products of a few rows with 4-bit weights ----------------------------------
+static_assert(MOE_MATVEC_MAX_ROWS <= moe::mv::kMaxRows, "the kernel keeps the rows' experts in shared memory");
+
 // Shared memory of a call.  Rows of x per tile: 8, or as many as fit beside two stages and
-// one buffer of scales.  Stages and scale buffers: what keeps two CTAs on an SM where that
-// fits, 2 to 4 stages and 1 or 2 buffers.  0 stages: does not fit.
+// one buffer of scales.  Then two buffers of scales if two stages stay, and stages in what
+// is left.  0 stages: does not fit.
 template <class T>
 moe::mv::Layout matvec_layout(int64_t R, int64_t K, int block, int limit) {
     namespace mv = moe::mv;
     mv::Layout L{};
     L.xs = mv::x_row_stride((int)K);
-    L.scale_bytes = (T::kRows * (int)(K / block) + 15 + 127) / 128 * 128;
+    L.rows = T::kRows;
+    L.scale_stride = (int)(K / block);
+    if (L.scale_stride % 32 == 0) L.scale_stride += 16;
+    L.scale_bytes = (T::kRows * (L.scale_stride + 4) + 8 + 15 + 127) / 128 * 128;
     const int factors = T::kFactorBytes * (block == 16 ? 2 : 1);
-    // the system's 1 KB, the way to a 1024-byte boundary, and rounding
-    const int fixed = T::kRedBytes + factors + (int)sizeof(mv::Shared) + 1024 + 1024 + 128;
+    // the way to a 1024-byte boundary, and rounding
+    const int fixed = T::kRedBytes + factors + (int)sizeof(mv::Shared) + 1024 + 128;
     const int64_t fit = ((int64_t)limit - fixed - L.scale_bytes - 2 * T::kStageBytes) / L.xs;
     L.nt = (int)std::min<int64_t>(std::min<int64_t>(mv::kTok, R), fit);
     if (L.nt < 1) return L;
     const int x_bytes = (L.nt * L.xs + 127) / 128 * 128;
-    for (const int room : {limit / T::kBlocksPerSm, limit}) {
-        for (L.scale_bufs = 2; L.scale_bufs >= 1; --L.scale_bufs) {
-            L.stages = std::min((room - fixed - x_bytes - L.scale_bufs * L.scale_bytes) / T::kStageBytes, mv::kMaxStages);
-            if (L.stages >= 2) break;
-        }
-        if (L.stages >= 2) break;
-    }
+    const int room = limit - fixed - x_bytes - L.scale_bytes;
+    L.scale_bufs = room - L.scale_bytes >= 2 * T::kStageBytes ? 2 : 1;
+    L.stages = std::min((room - (L.scale_bufs - 1) * L.scale_bytes) / T::kStageBytes, mv::kMaxStages);
     L.x = L.stages * T::kStageBytes;
     L.scales = L.x + x_bytes;
     L.red = L.scales + L.scale_bufs * L.scale_bytes;
@@ -865,26 +866,39 @@ int launch_matvec_tile(moe::mv::Params q, const uint8_t *blocks, int optin, cuda
     if (!make_matvec_map(&map, blocks, (int64_t)q.E * q.N, q.K, T::kRows)) return MOE_ERR_CUDA;
     auto kernel = mv::matvec_kernel<T, X, Out, kNv, kSwiGlu>;
     if (!ensure_smem_attr(reinterpret_cast<const void *>(kernel), q.L.total)) return MOE_ERR_CUDA;
-    const int per_sm = T::kBlocksPerSm * (q.L.total + (int)sizeof(mv::Shared) + 1024) <= optin + 1024 ? T::kBlocksPerSm : 1;
-    const int64_t grid = std::min<int64_t>(matvec_slots(q, q.L.nt) * moe::ceil_div(q.N, T::kRows),
-                                           (int64_t)sm_count() * per_sm);
+    const int64_t items = matvec_slots(q, q.L.nt) * moe::ceil_div(q.N, T::kRows);
+    const int64_t grid = std::min<int64_t>(items, sm_count());
     StageScope scope(kSwiGlu ? MOE_STAGE_GATE_UP : MOE_STAGE_DOWN, s);
     launch_pdl(kernel, dim3((unsigned)grid), dim3(T::kThreads), q.L.total, s, map, q);
     return launch_check();
 }
 
-#ifndef MOE_WIDE_ITEMS
-#define MOE_WIDE_ITEMS 4
-#endif
+// What a call costs with tile T, in weight rows of one SM at the rate of the tallest tile:
+// rounds of items over the SMs times an item's rows over the tile's rate.  A taller tile
+// spreads its bookkeeping over more rows, a lower one leaves fewer SMs idle in the last
+// round.  Rates measured on 1 GB of weights (gate_up of 64 tokens over 128 experts, us):
+// 128 rows 192, 64 rows 222, 32 rows 337.  The estimate picks the fastest of the three at
+// each size measured: one row of 2880 x 2880 9.2 / 7.2 / 6.3 us, one token's four experts
+// 18.3 / 16.3 / 18.5, eight tokens' down products 27.5 / 28.0 / 36.9.
+template <class T>
+double matvec_cost(const moe::mv::Params &q, int block, int optin, double rate) {
+    const moe::mv::Layout L = matvec_layout<T>(q.R, q.K, block, optin);
+    if (L.stages < 2) return 1e30;
+    const int64_t items = matvec_slots(q, L.nt) * moe::ceil_div(q.N, T::kRows);
+    return (double)moe::ceil_div(items, sm_count()) * T::kRows / rate;
+}
+
 template <class X, class Out, bool kNv, bool kSwiGlu>
 int launch_matvec(const moe::mv::Params &q, const uint8_t *blocks, cudaStream_t s) {
-    namespace mv = moe::mv;
-    const int optin = max_smem_optin();
-    const bool wide = matvec_slots(q, std::min(q.R, mv::kTok)) * moe::ceil_div(q.N, mv::WideTile::kRows) >=
-                          MOE_WIDE_ITEMS * sm_count() &&
-                      matvec_layout<mv::WideTile>(q.R, q.K, kNv ? 16 : 32, optin).stages >= 2;
-    return wide ? launch_matvec_tile<mv::WideTile, X, Out, kNv, kSwiGlu>(q, blocks, optin, s)
-                : launch_matvec_tile<mv::NarrowTile, X, Out, kNv, kSwiGlu>(q, blocks, optin, s);
+    using Tall = moe::mv::Tile<16, 4, 2, 4>;      // 128 rows x 512 elements a stage
+    using Middle = moe::mv::Tile<16, 8, 2, 4>;    // 64 x 1024
+    using Low = moe::mv::Tile<16, 16, 2, 2>;      // 32 x 1024
+    const int optin = max_smem_optin(), block = kNv ? 16 : 32;
+    const double tall = matvec_cost<Tall>(q, block, optin, 1.0), middle = matvec_cost<Middle>(q, block, optin, 0.87),
+                 low = matvec_cost<Low>(q, block, optin, 0.57);
+    if (tall <= middle && tall <= low && tall < 1e30) return launch_matvec_tile<Tall, X, Out, kNv, kSwiGlu>(q, blocks, optin, s);
+    if (middle <= low && middle < 1e30) return launch_matvec_tile<Middle, X, Out, kNv, kSwiGlu>(q, blocks, optin, s);
+    return launch_matvec_tile<Low, X, Out, kNv, kSwiGlu>(q, blocks, optin, s);
 }
 
 template <bool kNv>
