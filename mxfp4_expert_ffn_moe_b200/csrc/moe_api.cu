@@ -711,9 +711,34 @@ bool pair_sizes_ok(int64_t T, int64_t H, int k, int64_t R) {
            H < (int64_t(1) << 31);
 }
 
+// Shared memory of the bulk kernels: stages of at most 32 KB (the row split into equal
+// segments, multiples of 8 elements), 2 to 4 of them within 72 KB, so that three blocks
+// share an SM and some 170 KB are on their way to each.
+template <class Tok, class Row, int KM, bool kSum, bool kDot>
+int launch_bulk(const moe::PairRows &q, const void *a, int64_t a_stride, const void *rows_in, int64_t rows_stride, void *out,
+                int64_t out_stride, cudaStream_t s) {
+    const int64_t per_elem = ((!kSum || kDot) ? sizeof(Tok) : 0) + ((kSum || kDot) ? q.k * sizeof(Row) : 0);
+    const int64_t segs = moe::ceil_div(q.H * per_elem, 32 * 1024);
+    moe::PairBulk b{a, rows_in, out, a_stride, rows_stride, out_stride, 0, 0, 0};
+    b.seg = (int)(moe::ceil_div(moe::ceil_div(q.H, segs), 8) * 8);
+    b.stage_bytes = (int)((b.seg * per_elem + 127) / 128 * 128);
+    b.stages = (int)std::max<int64_t>(2, std::min<int64_t>(72 * 1024 / b.stage_bytes, moe::kBulkStages));
+    const int smem = b.stages * b.stage_bytes;
+    auto kernel = moe::pair_bulk_kernel<Tok, Row, KM, kSum, kDot>;
+    if (!ensure_smem_attr(reinterpret_cast<const void *>(kernel), smem)) return MOE_ERR_CUDA;
+    const int64_t per_sm = std::min<int64_t>(8, 227 * 1024 / (smem + 2048));
+    const int64_t grid = std::min<int64_t>(q.T, sm_count() * per_sm);
+    StageScope scope(kSum ? MOE_STAGE_COMBINE : MOE_STAGE_GATHER, s);
+    launch_pdl(kernel, dim3((unsigned)grid), dim3(moe::kBulkThreads), smem, s, q, b);
+    return launch_check();
+}
+
 template <class Tok, class Row, int VE, int KM, bool kDot>
 int launch_spread(moe::PairRows q, const void *a, int64_t a_stride, const void *src, int64_t src_stride, void *rows,
                   int64_t rows_stride, cudaStream_t s) {
+    if constexpr (VE == 8)
+        return launch_bulk<Tok, Row, KM, false, kDot>(q, a, a_stride, src, src_stride, rows, rows_stride, s);
+    else {
     q.group = pair_group(q.T, q.H / VE);
     const int64_t grid = moe::ceil_div(q.T, moe::kPairThreads / q.group);
     StageScope scope(MOE_STAGE_GATHER, s);
@@ -721,11 +746,15 @@ int launch_spread(moe::PairRows q, const void *a, int64_t a_stride, const void *
                static_cast<const Tok *>(a), a_stride, static_cast<const Row *>(src), src_stride,
                static_cast<Row *>(rows), rows_stride);
     return launch_check();
+    }
 }
 
 template <class Tok, class Row, int VE, int KM, bool kDot>
 int launch_sum(moe::PairRows q, const void *rows, int64_t rows_stride, const void *a, int64_t a_stride, void *out,
                int64_t out_stride, cudaStream_t s) {
+    if constexpr (VE == 8)
+        return launch_bulk<Tok, Row, KM, true, kDot>(q, a, a_stride, rows, rows_stride, out, out_stride, s);
+    else {
     q.group = pair_group(q.T, q.H / VE);
     const int64_t grid = moe::ceil_div(q.T, moe::kPairThreads / q.group);
     StageScope scope(MOE_STAGE_COMBINE, s);
@@ -733,6 +762,7 @@ int launch_sum(moe::PairRows q, const void *rows, int64_t rows_stride, const voi
                static_cast<const Row *>(rows), rows_stride, static_cast<const Tok *>(a), a_stride,
                static_cast<Tok *>(out), out_stride);
     return launch_check();
+    }
 }
 
 // Calls f(Tok{}, Row{}, VE, KM) of the compiled combinations: the token side and the
@@ -1146,11 +1176,10 @@ int moe_route_backward(const float *dweights, const int32_t *ids, const float *w
     if (!aligned(dweights, 4) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(dlogits, 4))
         return MOE_ERR_INVALID_ARG;
     cudaStream_t s = (cudaStream_t)stream;
-    const bool wide = E % 4 == 0 && aligned(dlogits, 16);
-    const int64_t per = 256 / (wide ? E / 4 : E);
+    const int64_t grid = moe::ceil_div(T, moe::route_grad_tokens((int)E));
     StageScope scope(MOE_STAGE_ROUTE, s);
-    launch_pdl(wide ? moe::route_backward_kernel<4> : moe::route_backward_kernel<1>,
-               dim3((unsigned)moe::ceil_div(T, per)), dim3(256), 0, s, dweights, ids, weights, T, (int)E, k, dlogits);
+    launch_pdl(aligned(dlogits, 16) ? moe::route_backward_kernel<true> : moe::route_backward_kernel<false>,
+               dim3((unsigned)grid), dim3(256), 0, s, dweights, ids, weights, T, (int)E, k, dlogits);
     return launch_check();
 }
 

@@ -87,50 +87,60 @@ __global__ void __launch_bounds__(256) route_topk_kernel(const float *__restrict
 // chosen logits, so dlogits[t, ids[t, j]] = w_j (dw_j - sum_i w_i dw_i), and the logits
 // that were not chosen do not move the weights: 0.  Empty slots (id -1) give nothing; an
 // expert named by two slots of a token gets both, in slot order.  Bound by the stores of
-// the dense [T, E] gradient: one thread per VE experts of a token, so each store is a
-// whole word and nothing is cleared first; a token's k pairs are read by its threads
-// through L1.
-template <int VE>
+// the dense [T, E] gradient.  A block builds the rows of `tokens` tokens in shared memory
+// (one thread per token and its k pairs) and stores them as one contiguous run of 16-byte
+// words: per word one shared load and one store, whatever k is.
+constexpr int kRouteGradFloats = 4096;     // of gradient per block (16 KB)
+__host__ __device__ constexpr int route_grad_tokens(int E) {
+    return kRouteGradFloats / E < 256 ? kRouteGradFloats / E / 4 * 4 : 256;
+}
+
+template <bool kWide>    // dlogits 16-byte aligned
 __global__ void __launch_bounds__(256) route_backward_kernel(const float *__restrict__ dweights,
                                                              const int32_t *__restrict__ ids,
                                                              const float *__restrict__ weights, int64_t T, int E,
                                                              int k, float *__restrict__ dlogits) {
+    __shared__ __align__(16) float grad[kRouteGradFloats];
+    const int tokens = route_grad_tokens(E), tid = threadIdx.x;
+    const int64_t t0 = (int64_t)blockIdx.x * tokens;
+    const int n = (int)min((int64_t)tokens, T - t0) * E;
     pdl_wait();
     pdl_trigger();
-    const unsigned q = (unsigned)E / VE, per = 256u / q;
-    const unsigned tl = threadIdx.x / q, c = threadIdx.x - tl * q;
-    const int64_t t = (int64_t)blockIdx.x * per + tl;
-    if (tl >= per || t >= T) return;
+    const bool mine = tid < tokens && t0 + tid < T;
     float w[8], g[8];
     int id[8];
-    float s = 0.0f;
+    if (mine) {
+        const int64_t p = (t0 + tid) * k;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (j >= k) break;
-        id[j] = __ldg(ids + t * k + j);
-        const bool used = id[j] >= 0 && id[j] < E;
-        if (!used && id[j] != -1) raise_device_error(MOE_DEVERR_BAD_EXPERT_ID);
-        if (!used) id[j] = -1;
-        w[j] = used ? __ldg(weights + t * k + j) : 0.0f;
-        g[j] = used ? __ldg(dweights + t * k + j) : 0.0f;
-        s = fmaf(w[j], g[j], s);
+        for (int j = 0; j < 8; ++j) {
+            id[j] = j < k ? __ldg(ids + p + j) : -1;
+            w[j] = j < k ? __ldg(weights + p + j) : 0.0f;
+            g[j] = j < k ? __ldg(dweights + p + j) : 0.0f;
+        }
     }
-    float o[VE];
+    for (int i = tid; i < (n + 3) / 4; i += 256) reinterpret_cast<float4 *>(grad)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+    if (mine) {
+        float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VE; ++i) o[i] = 0.0f;
+        for (int j = 0; j < 8; ++j) {
+            const bool used = id[j] >= 0 && id[j] < E;
+            if (!used && id[j] != -1) raise_device_error(MOE_DEVERR_BAD_EXPERT_ID);
+            if (!used) id[j] = -1;
+            if (used) s = fmaf(w[j], g[j], s);
+        }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (j >= k) break;
-        const float v = w[j] * (g[j] - s);
-#pragma unroll
-        for (int i = 0; i < VE; ++i)
-            if (id[j] == (int)(c * VE) + i) o[i] += v;
+        for (int j = 0; j < 8; ++j)
+            if (id[j] >= 0) grad[tid * E + id[j]] += w[j] * (g[j] - s);
     }
-    float *dst = dlogits + t * E + c * VE;
-    if constexpr (VE == 4)
-        *reinterpret_cast<float4 *>(dst) = make_float4(o[0], o[1], o[2], o[3]);
-    else
-        dst[0] = o[0];
+    __syncthreads();
+    float *dst = dlogits + t0 * E;       // tokens is a multiple of 4: 16-byte aligned if dlogits is
+    if constexpr (kWide) {
+        for (int i = tid; i < n / 4; i += 256) reinterpret_cast<float4 *>(dst)[i] = reinterpret_cast<const float4 *>(grad)[i];
+        if (tid < n % 4) dst[n / 4 * 4 + tid] = grad[n / 4 * 4 + tid];
+    } else {
+        for (int i = tid; i < n; i += 256) dst[i] = grad[i];
+    }
 }
 
 }  // namespace moe
