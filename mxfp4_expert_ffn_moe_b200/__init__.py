@@ -451,13 +451,19 @@ def moe_combine_pairs(y_rows, pair_rows, T: int, k: int, out=None, stream=None):
 
 # ---- training and few-token calls: bf16, fp16 and fp32, strided rows -----------------
 _DTYPE_CODES = {}
+_t = None           # torch, imported by the first call
+
+
+def _import_torch():
+    global _t
+    import torch
+    _DTYPE_CODES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    _t = torch
+    return torch
 
 
 def _dtype_code(dtype, name):
-    if not _DTYPE_CODES:
-        import torch
-        _DTYPE_CODES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
-    code = _DTYPE_CODES.get(dtype)
+    code = (_DTYPE_CODES or (_import_torch() and _DTYPE_CODES)).get(dtype)
     if code is None:
         raise ValueError(f"{name}: expected bfloat16, float16 or float32, got {dtype}")
     return code
@@ -467,14 +473,13 @@ class _Call:
     """Argument marshalling of one call: every tensor on the current CUDA device, outputs
     allocated for the stream the call runs on, and tensors used on a stream other than
     the current one kept from the allocator until that stream has run the call.  A decode
-    step makes many such calls, so this is kept short: raw stream and device handles, one
-    pass over each tensor's properties."""
+    step makes many such calls of a few microseconds each, so this is kept short: raw
+    stream and device handles, one pass over each tensor's properties."""
 
-    __slots__ = ("torch", "device", "side", "stream")
+    __slots__ = ("device", "side", "stream")
 
     def __init__(self, like, stream):
-        import torch
-        self.torch = torch
+        torch = _t or _import_torch()
         self.device = like.get_device()
         if self.device < 0 or self.device != torch._C._cuda_getDevice():
             raise ValueError(f"expected tensors on the current CUDA device, got one on {like.device}")
@@ -487,35 +492,34 @@ class _Call:
     def empty(self, like, shape, dtype):
         if self.side is None:
             return like.new_empty(shape, dtype=dtype)
-        with self.torch.cuda.stream(self.side):
+        with _t.cuda.stream(self.side):
             return like.new_empty(shape, dtype=dtype)
-
-    def _use(self, t, name):
-        if t.get_device() != self.device:
-            raise ValueError(f"{name}: on {t.device}, expected cuda:{self.device}")
-        if self.side is not None:
-            t.record_stream(self.side)
 
     def flat(self, t, dtype, name, numel):
         """Contiguous tensor of `numel` elements (None stays None)."""
         if t is None:
             return None
-        if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous():
-            raise ValueError(f"{name}: expected a contiguous {dtype} tensor of {numel} elements, got "
-                             f"{t.dtype} {tuple(t.shape)} (contiguous={t.is_contiguous()})")
-        self._use(t, name)
+        if t.dtype is not dtype or t.numel() != numel or t.get_device() != self.device or not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous {dtype} tensor of {numel} elements on cuda:{self.device}, "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
+        if self.side is not None:
+            t.record_stream(self.side)
         return t.data_ptr()
 
-    def rows(self, t, name, shape, dtype=None):
-        """2-D tensor of contiguous rows, any row stride: (pointer, dtype code, stride)."""
+    def rows(self, t, name, n, width, dtype=None):
+        """2-D tensor [n, width] of contiguous rows, any row stride: (pointer, dtype code, stride)."""
         if t is None:
             return None, 0, 0
-        code = _dtype_code(t.dtype, name)
-        if t.shape != shape or (dtype is not None and t.dtype is not dtype) or (shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError(f"{name}: expected {shape}{'' if dtype is None else f' of {dtype}'} with contiguous rows, "
-                             f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
-        self._use(t, name)
-        return t.data_ptr(), code, t.stride(0) if shape[0] > 1 else shape[1]
+        code = _DTYPE_CODES.get(t.dtype)
+        stride = t.stride()
+        if (code is None or t.shape != (n, width) or t.get_device() != self.device or (dtype is not None and
+                t.dtype is not dtype) or (stride[1] != 1 and width > 1)):
+            raise ValueError(f"{name}: expected a [{n}, {width}] tensor of {dtype or 'bfloat16, float16 or float32'} with "
+                             f"contiguous rows on cuda:{self.device}, got {t.dtype} {tuple(t.shape)} on {t.device} with "
+                             f"strides {stride}")
+        if self.side is not None:
+            t.record_stream(self.side)
+        return t.data_ptr(), code, stride[0] if n > 1 else width
 
 
 def moe_dispatch_rows(x, pair_rows, k: int, weights=None, n_rows: Optional[int] = None, dtype=None, rows=None,
@@ -529,11 +533,14 @@ def moe_dispatch_rows(x, pair_rows, k: int, weights=None, n_rows: Optional[int] 
     T, H = x.shape
     if rows is None:
         rows = c.empty(x, (T * k if n_rows is None else n_rows, H), dtype or x.dtype)
-    xp, xd, xs = c.rows(x, "x", (T, H))
-    rp, rd, rs = c.rows(rows, "rows", (rows.shape[0], H), dtype)
-    _check("moe_dispatch_rows", load_library().moe_dispatch_rows(
-        xp, xd, xs, T, H, int(k), c.flat(pair_rows, c.torch.int32, "pair_rows", T * k),
-        c.flat(weights, c.torch.float32, "weights", T * k), rows.shape[0], rp, rd, rs, c.stream))
+    R = rows.shape[0]
+    xp, xd, xs = c.rows(x, "x", T, H)
+    rp, rd, rs = c.rows(rows, "rows", R, H, dtype)
+    rc = (_lib or load_library()).moe_dispatch_rows(
+        xp, xd, xs, T, H, k, c.flat(pair_rows, _t.int32, "pair_rows", T * k),
+        c.flat(weights, _t.float32, "weights", T * k), R, rp, rd, rs, c.stream)
+    if rc:
+        raise MoEError("moe_dispatch_rows", rc)
     return rows
 
 
@@ -546,15 +553,19 @@ def moe_dispatch_rows_backward(drows, pair_rows, T: int, k: int, weights=None, x
     R, H = drows.shape
     if dx is None:
         dx = c.empty(drows, (T, H), dtype or (drows.dtype if x is None else x.dtype))
-    if x is not None and dweights is None:
-        dweights = c.empty(drows, (T, k), c.torch.float32)
-    rp, rd, rs = c.rows(drows, "drows", (R, H))
-    dp, dd, ds = c.rows(dx, "dx", (T, H), dtype)
-    xp, _, xs = c.rows(x, "x", (T, H), dx.dtype)
-    _check("moe_dispatch_rows_backward", load_library().moe_dispatch_rows_backward(
-        rp, rd, rs, T, H, int(k), R, c.flat(pair_rows, c.torch.int32, "pair_rows", T * k),
-        c.flat(weights, c.torch.float32, "weights", T * k), xp, xs, dp, dd, ds,
-        c.flat(dweights, c.torch.float32, "dweights", T * k), c.stream))
+    if x is None:
+        dweights = None
+    elif dweights is None:
+        dweights = c.empty(drows, (T, k), _t.float32)
+    rp, rd, rs = c.rows(drows, "drows", R, H)
+    dp, dd, ds = c.rows(dx, "dx", T, H, dtype)
+    xp, _, xs = c.rows(x, "x", T, H, dx.dtype)
+    rc = (_lib or load_library()).moe_dispatch_rows_backward(
+        rp, rd, rs, T, H, k, R, c.flat(pair_rows, _t.int32, "pair_rows", T * k),
+        c.flat(weights, _t.float32, "weights", T * k), xp, xs, dp, dd, ds,
+        c.flat(dweights, _t.float32, "dweights", T * k), c.stream)
+    if rc:
+        raise MoEError("moe_dispatch_rows_backward", rc)
     return dx if x is None else (dx, dweights)
 
 
@@ -567,11 +578,13 @@ def moe_combine_rows(rows, pair_rows, T: int, k: int, weights=None, dtype=None, 
     R, H = rows.shape
     if out is None:
         out = c.empty(rows, (T, H), dtype or rows.dtype)
-    rp, rd, rs = c.rows(rows, "rows", (R, H))
-    op, od, os_ = c.rows(out, "out", (T, H), dtype)
-    _check("moe_combine_rows", load_library().moe_combine_rows(
-        rp, rd, rs, T, H, int(k), R, c.flat(pair_rows, c.torch.int32, "pair_rows", T * k),
-        c.flat(weights, c.torch.float32, "weights", T * k), op, od, os_, c.stream))
+    rp, rd, rs = c.rows(rows, "rows", R, H)
+    op, od, os_ = c.rows(out, "out", T, H, dtype)
+    rc = (_lib or load_library()).moe_combine_rows(
+        rp, rd, rs, T, H, k, R, c.flat(pair_rows, _t.int32, "pair_rows", T * k),
+        c.flat(weights, _t.float32, "weights", T * k), op, od, os_, c.stream)
+    if rc:
+        raise MoEError("moe_combine_rows", rc)
     return out
 
 
@@ -588,15 +601,19 @@ def moe_combine_rows_backward(dout, pair_rows, k: int, weights=None, y_rows=None
         n = y_rows.shape[0] if y_rows is not None else T * k if n_rows is None else n_rows
         drows = c.empty(dout, (n, H), dtype or (dout.dtype if y_rows is None else y_rows.dtype))
     R = drows.shape[0]
-    if y_rows is not None and dweights is None:
-        dweights = c.empty(dout, (T, k), c.torch.float32)
-    op, od, os_ = c.rows(dout, "dout", (T, H))
-    dp, dd, ds = c.rows(drows, "drows", (R, H), dtype)
-    yp, _, ys = c.rows(y_rows, "y_rows", (R, H), drows.dtype)
-    _check("moe_combine_rows_backward", load_library().moe_combine_rows_backward(
-        op, od, os_, T, H, int(k), c.flat(pair_rows, c.torch.int32, "pair_rows", T * k),
-        c.flat(weights, c.torch.float32, "weights", T * k), yp, ys, R, dp, dd, ds,
-        c.flat(dweights, c.torch.float32, "dweights", T * k), c.stream))
+    if y_rows is None:
+        dweights = None
+    elif dweights is None:
+        dweights = c.empty(dout, (T, k), _t.float32)
+    op, od, os_ = c.rows(dout, "dout", T, H)
+    dp, dd, ds = c.rows(drows, "drows", R, H, dtype)
+    yp, _, ys = c.rows(y_rows, "y_rows", R, H, drows.dtype)
+    rc = (_lib or load_library()).moe_combine_rows_backward(
+        op, od, os_, T, H, k, c.flat(pair_rows, _t.int32, "pair_rows", T * k),
+        c.flat(weights, _t.float32, "weights", T * k), yp, ys, R, dp, dd, ds,
+        c.flat(dweights, _t.float32, "dweights", T * k), c.stream)
+    if rc:
+        raise MoEError("moe_combine_rows_backward", rc)
     return drows if y_rows is None else (drows, dweights)
 
 
@@ -606,40 +623,43 @@ def moe_route_backward(dweights, ids, weights, E: int, dlogits=None, stream=None
     c = _Call(dweights, stream)
     T, k = dweights.shape
     if dlogits is None:
-        dlogits = c.empty(dweights, (T, E), c.torch.float32)
-    _check("moe_route_backward", load_library().moe_route_backward(
-        c.flat(dweights, c.torch.float32, "dweights", T * k), c.flat(ids, c.torch.int32, "ids", T * k),
-        c.flat(weights, c.torch.float32, "weights", T * k), T, int(E), k,
-        c.flat(dlogits, c.torch.float32, "dlogits", T * E), c.stream))
+        dlogits = c.empty(dweights, (T, E), _t.float32)
+    f32 = _t.float32
+    rc = (_lib or load_library()).moe_route_backward(
+        c.flat(dweights, f32, "dweights", T * k), c.flat(ids, _t.int32, "ids", T * k),
+        c.flat(weights, f32, "weights", T * k), T, E, k, c.flat(dlogits, f32, "dlogits", T * E), c.stream)
+    if rc:
+        raise MoEError("moe_route_backward", rc)
     return dlogits
 
 
 def _matvec(name, block, x, blocks, scales, scale2, bias, row_ids, rows_per_x, swiglu, alpha, limit, out_dtype, out,
             stream):
     c = _Call(x, stream)
-    torch = c.torch
     Tx, K = x.shape
     E, N, Kh = blocks.shape if blocks.dim() == 3 else (1, *blocks.shape)
     if Kh * 2 != K:
         raise ValueError(f"{name}: x has {K} columns, the weights {2 * Kh}")
     R = Tx * rows_per_x if row_ids is None else row_ids.numel()
-    if -(-R // rows_per_x) != Tx:
+    if rows_per_x < 1 or -(-R // rows_per_x) != Tx:
         raise ValueError(f"{name}: {R} rows at {rows_per_x} per row of x do not make the {Tx} rows of x")
-    shape = (R, N // 2 if swiglu else N)
+    n_out = N // 2 if swiglu else N
     if out is None:
-        out = c.empty(x, shape, out_dtype or x.dtype)
-    if not out.is_contiguous():
+        out = c.empty(x, (R, n_out), out_dtype or x.dtype)
+    elif not out.is_contiguous():
         raise ValueError("out: expected a contiguous tensor")
-    xp, xd, xs = c.rows(x, "x", (Tx, K))
-    op, od, _ = c.rows(out, "out", shape, out_dtype)
-    args = [xp, xd, xs, int(rows_per_x), R, N, K, E, c.flat(row_ids, torch.int32, "row_ids", R),
-            c.flat(blocks, torch.uint8, "blocks", E * N * Kh),
-            c.flat(scales, torch.uint8, "scales", E * N * (K // block))]
+    u8, f32 = _t.uint8, _t.float32
+    xp, xd, xs = c.rows(x, "x", Tx, K)
+    op, od, _ = c.rows(out, "out", R, n_out, out_dtype)
+    args = [xp, xd, xs, rows_per_x, R, N, K, E, c.flat(row_ids, _t.int32, "row_ids", R),
+            c.flat(blocks, u8, "blocks", E * N * Kh), c.flat(scales, u8, "scales", E * N * (K // block))]
     if block == 16:
-        args.append(c.flat(scale2, torch.float32, "scale2", 2 * E if swiglu else E))
-    args += [c.flat(bias, torch.float32, "bias", E * N), MOE_FLAG_SWIGLU if swiglu else 0, float(alpha), float(limit),
-             op, od, c.stream]
-    _check(name, getattr(load_library(), name)(*args))
+        args.append(c.flat(scale2, f32, "scale2", 2 * E if swiglu else E))
+    args += (c.flat(bias, f32, "bias", E * N), MOE_FLAG_SWIGLU if swiglu else 0, alpha, limit, op, od, c.stream)
+    lib = _lib or load_library()
+    rc = (lib.mxfp4_matvec if block == 32 else lib.nvfp4_matvec)(*args)
+    if rc:
+        raise MoEError(name, rc)
     return out
 
 

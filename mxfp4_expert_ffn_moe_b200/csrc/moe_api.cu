@@ -683,27 +683,12 @@ struct RowsArg {
     size_t size;
 };
 
-// Elements per chunk: 8 (16-byte words) when every row of every operand starts on a
-// 16-byte boundary and H is a multiple of 8; else 2 under the same rule for two
-// elements; else 1.
-int chunk_elems(int64_t H, std::initializer_list<RowsArg> rows) {
-    for (const int ve : {8, 2}) {
-        bool ok = H % ve == 0;
-        for (const RowsArg &a : rows) {
-            const size_t word = std::min<size_t>(16, ve * a.size);
-            ok = ok && (!a.p || (aligned(a.p, word) && (a.stride * (int64_t)a.size) % (int64_t)word == 0));
-        }
-        if (ok) return ve;
-    }
-    return 1;
-}
-
-// Threads per token: 32 (a warp) once the tokens alone give every SM 32 warps, up to a
-// whole block of 256 below that, and no more than the row has chunks for.
-int pair_group(int64_t T, int64_t chunks) {
-    int g = 32;
-    while (g < moe::kPairThreads && T * g < (int64_t)sm_count() * 1024 && g < chunks) g *= 2;
-    return g;
+// Whether every row of every operand lies on 16-byte words (pairs of them for fp32 rows
+// beside two-byte ones: chunks are 8 elements of each).
+bool rows_of_words(int64_t H, std::initializer_list<RowsArg> rows) {
+    bool ok = H % 8 == 0;
+    for (const RowsArg &a : rows) ok = ok && (!a.p || (aligned(a.p, 16) && (a.stride * (int64_t)a.size) % 16 == 0));
+    return ok;
 }
 
 bool pair_sizes_ok(int64_t T, int64_t H, int k, int64_t R) {
@@ -711,20 +696,21 @@ bool pair_sizes_ok(int64_t T, int64_t H, int k, int64_t R) {
            H < (int64_t(1) << 31);
 }
 
-// Shared memory of the bulk kernels: stages of at most 32 KB (the row split into equal
-// segments, multiples of 8 elements), 2 to 4 of them within 72 KB, so that three blocks
-// share an SM and some 170 KB are on their way to each.
-template <class Tok, class Row, int KM, bool kSum, bool kDot>
-int launch_bulk(const moe::PairRows &q, const void *a, int64_t a_stride, const void *rows_in, int64_t rows_stride, void *out,
-                int64_t out_stride, cudaStream_t s) {
-    const int64_t per_elem = ((!kSum || kDot) ? sizeof(Tok) : 0) + ((kSum || kDot) ? q.k * sizeof(Row) : 0);
-    const int64_t segs = moe::ceil_div(q.H * per_elem, 32 * 1024);
-    moe::PairBulk b{a, rows_in, out, a_stride, rows_stride, out_stride, 0, 0, 0};
+// Shared memory: stages of at most 32 KB (the row split into equal segments, multiples of 8
+// elements), 2 to 4 of them within 72 KB, so that three blocks share an SM and some 170 KB
+// are on their way to each.  Off 16-byte words a row takes up to 30 bytes more.
+template <class Tok, class Row, int KM, bool kSum, bool kDot, bool kWords>
+int launch_pairs(const moe::PairRows &q, moe::PairBulk b, cudaStream_t s) {
+    const int64_t tok = (!kSum || kDot) ? sizeof(Tok) : 0, row = (kSum || kDot) ? sizeof(Row) : 0;
+    const int64_t segs = moe::ceil_div(q.H * (tok + q.k * row), 32 * 1024);
     b.seg = (int)(moe::ceil_div(moe::ceil_div(q.H, segs), 8) * 8);
-    b.stage_bytes = (int)((b.seg * per_elem + 127) / 128 * 128);
-    b.stages = (int)std::max<int64_t>(2, std::min<int64_t>(72 * 1024 / b.stage_bytes, moe::kBulkStages));
+    const auto slot = [&](int64_t size) { return (int)(size ? (b.seg * size + 15) / 16 * 16 + (kWords ? 0 : 16) : 0); };
+    b.a_slot = slot(tok);
+    b.row_slot = slot(row);
+    b.stage_bytes = (b.a_slot + q.k * b.row_slot + 127) / 128 * 128;
+    b.stages = std::max(2, std::min(72 * 1024 / b.stage_bytes, moe::kBulkStages));
     const int smem = b.stages * b.stage_bytes;
-    auto kernel = moe::pair_bulk_kernel<Tok, Row, KM, kSum, kDot>;
+    auto kernel = moe::pair_bulk_kernel<Tok, Row, KM, kSum, kDot, kWords>;
     if (!ensure_smem_attr(reinterpret_cast<const void *>(kernel), smem)) return MOE_ERR_CUDA;
     const int64_t per_sm = std::min<int64_t>(8, 227 * 1024 / (smem + 2048));
     const int64_t grid = std::min<int64_t>(q.T, sm_count() * per_sm);
@@ -733,61 +719,49 @@ int launch_bulk(const moe::PairRows &q, const void *a, int64_t a_stride, const v
     return launch_check();
 }
 
-template <class Tok, class Row, int VE, int KM, bool kDot>
-int launch_spread(moe::PairRows q, const void *a, int64_t a_stride, const void *src, int64_t src_stride, void *rows,
-                  int64_t rows_stride, cudaStream_t s) {
-    if constexpr (VE == 8)
-        return launch_bulk<Tok, Row, KM, false, kDot>(q, a, a_stride, src, src_stride, rows, rows_stride, s);
-    else {
-    q.group = pair_group(q.T, q.H / VE);
-    const int64_t grid = moe::ceil_div(q.T, moe::kPairThreads / q.group);
+// Unweighted rows of one type on 16-byte words: segments of at most 8 KB, four of them a
+// warp, three warps an SM (8192 tokens x 4 rows of 2880 bf16, 1 / 3 / 6 / 12 warps: 59, 45, 51,
+// 52 us; more rows written at once do not help DRAM).  The general kernel takes 48.7 us.
+int launch_copy(const moe::PairRows &q, moe::PairBulk b, int elem, cudaStream_t s) {
+    const int64_t segs = moe::ceil_div(q.H * elem, 8 * 1024);
+    b.seg = (int)(moe::ceil_div(moe::ceil_div(q.H, segs), 8) * 8);
+    b.stage_bytes = (b.seg * elem + 127) / 128 * 128;
+    b.stages = moe::kCopyStages;
+    const int smem = b.stages * b.stage_bytes;
+    if (!ensure_smem_attr(reinterpret_cast<const void *>(moe::copy_rows_kernel), smem)) return MOE_ERR_CUDA;
+    const int64_t grid = std::min<int64_t>(q.T, sm_count() * 3);
     StageScope scope(MOE_STAGE_GATHER, s);
-    launch_pdl(moe::spread_rows_kernel<Tok, Row, VE, KM, kDot>, dim3((unsigned)grid), dim3(moe::kPairThreads), 0, s, q,
-               static_cast<const Tok *>(a), a_stride, static_cast<const Row *>(src), src_stride,
-               static_cast<Row *>(rows), rows_stride);
+    launch_pdl(moe::copy_rows_kernel, dim3((unsigned)grid), dim3(32), smem, s, q, b, elem);
     return launch_check();
-    }
 }
 
-template <class Tok, class Row, int VE, int KM, bool kDot>
-int launch_sum(moe::PairRows q, const void *rows, int64_t rows_stride, const void *a, int64_t a_stride, void *out,
-               int64_t out_stride, cudaStream_t s) {
-    if constexpr (VE == 8)
-        return launch_bulk<Tok, Row, KM, true, kDot>(q, a, a_stride, rows, rows_stride, out, out_stride, s);
-    else {
-    q.group = pair_group(q.T, q.H / VE);
-    const int64_t grid = moe::ceil_div(q.T, moe::kPairThreads / q.group);
-    StageScope scope(MOE_STAGE_COMBINE, s);
-    launch_pdl(moe::sum_rows_kernel<Tok, Row, VE, KM, kDot>, dim3((unsigned)grid), dim3(moe::kPairThreads), 0, s, q,
-               static_cast<const Row *>(rows), rows_stride, static_cast<const Tok *>(a), a_stride,
-               static_cast<Tok *>(out), out_stride);
-    return launch_check();
-    }
-}
-
-// Calls f(Tok{}, Row{}, VE, KM) of the compiled combinations: the token side and the
-// expert side of one type, or fp32 expert rows.
+// Calls f(Tok{}, Row{}, KM) of the compiled combinations: the token side and the expert side
+// of one type, or fp32 expert rows; up to 4 or 8 pairs a token.
 template <int N>
 using Int = std::integral_constant<int, N>;
-template <class Tok, class Row, class F>
-int with_shape(int ve, int k, F &&f) {
-    if (k <= 4) {
-        if (ve == 8) return f(Tok{}, Row{}, Int<8>{}, Int<4>{});
-        if (ve == 2) return f(Tok{}, Row{}, Int<2>{}, Int<4>{});
-        return f(Tok{}, Row{}, Int<1>{}, Int<4>{});
-    }
-    if (ve == 8) return f(Tok{}, Row{}, Int<8>{}, Int<8>{});
-    if (ve == 2) return f(Tok{}, Row{}, Int<2>{}, Int<8>{});
-    return f(Tok{}, Row{}, Int<1>{}, Int<8>{});
-}
 template <class F>
-int with_types(int tok, int row, int ve, int k, F &&f) {
-    if (tok == MOE_DTYPE_BF16 && row == MOE_DTYPE_BF16) return with_shape<__nv_bfloat16, __nv_bfloat16>(ve, k, f);
-    if (tok == MOE_DTYPE_F16 && row == MOE_DTYPE_F16) return with_shape<__half, __half>(ve, k, f);
-    if (tok == MOE_DTYPE_F32 && row == MOE_DTYPE_F32) return with_shape<float, float>(ve, k, f);
-    if (tok == MOE_DTYPE_BF16 && row == MOE_DTYPE_F32) return with_shape<__nv_bfloat16, float>(ve, k, f);
-    if (tok == MOE_DTYPE_F16 && row == MOE_DTYPE_F32) return with_shape<__half, float>(ve, k, f);
+int with_types(int tok, int row, int k, F &&f) {
+    const auto with_k = [&](auto t, auto r) { return k <= 4 ? f(t, r, Int<4>{}) : f(t, r, Int<8>{}); };
+    if (tok == MOE_DTYPE_BF16 && row == MOE_DTYPE_BF16) return with_k(__nv_bfloat16{}, __nv_bfloat16{});
+    if (tok == MOE_DTYPE_F16 && row == MOE_DTYPE_F16) return with_k(__half{}, __half{});
+    if (tok == MOE_DTYPE_F32 && row == MOE_DTYPE_F32) return with_k(float{}, float{});
+    if (tok == MOE_DTYPE_BF16 && row == MOE_DTYPE_F32) return with_k(__nv_bfloat16{}, float{});
+    if (tok == MOE_DTYPE_F16 && row == MOE_DTYPE_F32) return with_k(__half{}, float{});
     return MOE_ERR_UNSUPPORTED;
+}
+
+template <bool kSum>
+int run_pairs(const moe::PairRows &q, const moe::PairBulk &b, int tok, int row, bool words, cudaStream_t s) {
+    return with_types(tok, row, q.k, [&](auto t, auto r, auto km) {
+        using Tok = decltype(t);
+        using Row = decltype(r);
+        constexpr int KM = decltype(km)::value;
+        if (q.dots)
+            return words ? launch_pairs<Tok, Row, KM, kSum, true, true>(q, b, s)
+                         : launch_pairs<Tok, Row, KM, kSum, true, false>(q, b, s);
+        return words ? launch_pairs<Tok, Row, KM, kSum, false, true>(q, b, s)
+                     : launch_pairs<Tok, Row, KM, kSum, false, false>(q, b, s);
+    });
 }
 
 // rows[r(p)] = s_p a[t]; with src: dots[p] = <a[t], src[r(p)]>.
@@ -801,16 +775,13 @@ int spread(const void *a, int a_dtype, int64_t a_stride, int64_t T, int64_t H, i
     if (!aligned(a, dtype_size(a_dtype)) || !aligned(src, dtype_size(rows_dtype)) ||
         !aligned(rows, dtype_size(rows_dtype)) || !aligned(pair_rows, 4) || !aligned(weights, 4) || !aligned(dots, 4))
         return MOE_ERR_INVALID_ARG;
-    const moe::PairRows q{T, H, R, k, 0, pair_rows, weights, dots};
-    const int ve = chunk_elems(H, {{a, a_stride, dtype_size(a_dtype)},
-                                   {src, src_stride, dtype_size(rows_dtype)},
-                                   {rows, rows_stride, dtype_size(rows_dtype)}});
-    return with_types(a_dtype, rows_dtype, ve, k, [&](auto tok, auto row, auto v, auto km) {
-        using Tok = decltype(tok);
-        using Row = decltype(row);
-        return src ? launch_spread<Tok, Row, v.value, km.value, true>(q, a, a_stride, src, src_stride, rows, rows_stride, s)
-                   : launch_spread<Tok, Row, v.value, km.value, false>(q, a, a_stride, src, src_stride, rows, rows_stride, s);
-    });
+    const moe::PairRows q{T, H, R, k, pair_rows, weights, dots};
+    const moe::PairBulk b{a, src, rows, a_stride, src_stride, rows_stride, 0, 0, 0, 0, 0};
+    const bool words = rows_of_words(H, {{a, a_stride, dtype_size(a_dtype)},
+                                         {src, src_stride, dtype_size(rows_dtype)},
+                                         {rows, rows_stride, dtype_size(rows_dtype)}});
+    if (words && !weights && !dots && a_dtype == rows_dtype) return launch_copy(q, b, (int)dtype_size(a_dtype), s);
+    return run_pairs<false>(q, b, a_dtype, rows_dtype, words, s);
 }
 
 // out[t] = sum_j s_p rows[r(p)]; with a: dots[p] = <a[t], rows[r(p)]>.
@@ -824,16 +795,12 @@ int sum_rows(const void *rows, int rows_dtype, int64_t rows_stride, int64_t T, i
     if (!aligned(rows, dtype_size(rows_dtype)) || !aligned(a, dtype_size(out_dtype)) ||
         !aligned(out, dtype_size(out_dtype)) || !aligned(pair_rows, 4) || !aligned(weights, 4) || !aligned(dots, 4))
         return MOE_ERR_INVALID_ARG;
-    const moe::PairRows q{T, H, R, k, 0, pair_rows, weights, dots};
-    const int ve = chunk_elems(H, {{rows, rows_stride, dtype_size(rows_dtype)},
-                                   {a, a_stride, dtype_size(out_dtype)},
-                                   {out, out_stride, dtype_size(out_dtype)}});
-    return with_types(out_dtype, rows_dtype, ve, k, [&](auto tok, auto row, auto v, auto km) {
-        using Tok = decltype(tok);
-        using Row = decltype(row);
-        return a ? launch_sum<Tok, Row, v.value, km.value, true>(q, rows, rows_stride, a, a_stride, out, out_stride, s)
-                 : launch_sum<Tok, Row, v.value, km.value, false>(q, rows, rows_stride, a, a_stride, out, out_stride, s);
-    });
+    const moe::PairRows q{T, H, R, k, pair_rows, weights, dots};
+    const moe::PairBulk b{a, rows, out, a_stride, rows_stride, out_stride, 0, 0, 0, 0, 0};
+    const bool words = rows_of_words(H, {{rows, rows_stride, dtype_size(rows_dtype)},
+                                         {a, a_stride, dtype_size(out_dtype)},
+                                         {out, out_stride, dtype_size(out_dtype)}});
+    return run_pairs<true>(q, b, out_dtype, rows_dtype, words, s);
 }
 
 // ---- products of a few rows with 4-bit weights ----------------------------------

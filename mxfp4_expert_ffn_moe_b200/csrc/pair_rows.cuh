@@ -15,10 +15,11 @@
 // tokens, not the expert rows: a token's row is then read (written) once instead of k
 // times, and its k expert rows are whole contiguous runs wherever they lie.
 //
-// Two kernels for each.  Rows of 16-byte words (the usual case) come through shared memory
-// by bulk asynchronous copies, a copy per row, issued by a warp of their own a token or two
-// ahead: what is in flight is then a matter of shared memory, not of registers and warps.
-// Any other rows are read directly, two elements or one at a time.
+// Rows come through shared memory by bulk asynchronous copies, a copy per row, issued by a
+// warp of their own a token or two ahead: what is in flight is then a matter of shared
+// memory, not of registers and warps.  Rows that do not lie on 16-byte words come as the
+// 16-byte granules that hold them and are taken apart element by element; the granules at
+// the two ends of a tensor, which may not be its own, are read with plain loads.
 #pragma once
 #include <cuda_fp16.h>
 
@@ -26,8 +27,6 @@
 #include "sm100_ptx.cuh"
 
 namespace moe {
-
-constexpr int kPairThreads = 256;
 
 // ---- VE elements of a row as fp32 --------------------------------------------------
 __device__ __forceinline__ float elem_to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -43,7 +42,7 @@ template <>
 __device__ __forceinline__ float f32_to_elem<float>(float v) { return v; }
 
 // VE consecutive elements as they lie in memory: one 16-byte word (8 two-byte elements),
-// two (8 floats), or one word of 2 or 1 elements.
+// two (8 floats), or a single element.
 template <class T, int VE>
 struct Chunk {
     static constexpr int kBytes = VE * (int)sizeof(T);
@@ -54,17 +53,6 @@ struct Chunk {
     };
     Word w[kWords];
     __device__ __forceinline__ void load(const T *p) {
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-            if constexpr (kWord == 16) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
-                w[i] = *reinterpret_cast<const Word *>(&v);
-            } else {
-                w[i] = reinterpret_cast<const Word *>(p)[i];
-            }
-        }
-    }
-    __device__ __forceinline__ void load_shared(const T *p) {
 #pragma unroll
         for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const Word *>(p)[i];
     }
@@ -82,194 +70,70 @@ struct Chunk {
     }
 };
 
-// What both kernels take.  Strides are in elements.
+// What the kernels take.
 struct PairRows {
     int64_t T, H, R;
     int k;
-    int group;                  // threads per token: 32 .. 256, a power of two
     const int32_t *pair_rows;   // [T*k] or null
     const float *weights;       // [T*k] or null
     float *dots;                // [T*k] (kDot)
 };
 
-// The expert rows and weights of one token; a dropped pair gets row -1.  A row past the
-// R rows of the buffer is dropped too and flagged.
-template <int KM>
-__device__ __forceinline__ void load_pairs(const PairRows &q, int64_t t, int (&row)[KM], float (&s)[KM]) {
-#pragma unroll
-    for (int j = 0; j < KM; ++j) {
-        row[j] = -1;
-        s[j] = 1.0f;
-        if (j < q.k) {
-            const int64_t p = t * q.k + j;
-            const int64_t r = q.pair_rows ? (int64_t)__ldg(q.pair_rows + p) : p;
-            if (r >= q.R)
-                raise_device_error(MOE_DEVERR_OUT_OF_BOUNDS);
-            else
-                row[j] = r < 0 ? -1 : (int)r;
-            if (q.weights) s[j] = __ldg(q.weights + p);
-        }
-    }
-}
-
-// Sum of each dot over the token's `group` threads, written by its first thread.  Called
-// by all threads of the block.
-template <int KM>
-__device__ __forceinline__ void write_dots(const PairRows &q, int64_t t, bool live, float (&dot)[KM]) {
-    __shared__ float part[kPairThreads / 32][KM];
-#pragma unroll
-    for (int j = 0; j < KM; ++j)
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], d);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0)
-#pragma unroll
-        for (int j = 0; j < KM; ++j) part[warp][j] = dot[j];
-    __syncthreads();
-    const int local = threadIdx.x & (q.group - 1);
-    if (live && local < q.k) {
-        float v = 0.0f;
-        for (int w = 0; w < q.group / 32; ++w) v += part[warp + w][local];   // local < 32: warp is the group's first
-        q.dots[t * q.k + local] = v;
-    }
-}
-
-// Chunks of a row that a thread has in flight at once, with KM expert rows each, and the
-// blocks of 256 threads that keep an SM supplied with them: registers are capped to let
-// kPairBlocks blocks on an SM.
-__host__ __device__ constexpr int pair_unroll(int VE, int KM) { return VE == 8 ? 1 : (VE == 2 ? 16 : 32) / KM; }
-constexpr int pair_blocks(int KM) { return KM == 4 ? 4 : 2; }
-
-template <class Tok, class Row, int VE, int KM, bool kDot>
-__global__ void __launch_bounds__(kPairThreads, pair_blocks(KM)) spread_rows_kernel(PairRows q, const Tok *__restrict__ a,
-                                                                   int64_t a_stride, const Row *__restrict__ src,
-                                                                   int64_t src_stride, Row *__restrict__ rows,
-                                                                   int64_t rows_stride) {
-    pdl_wait();
-    pdl_trigger();
-    const int64_t t = (int64_t)blockIdx.x * (kPairThreads / q.group) + threadIdx.x / q.group;
-    const int local = threadIdx.x & (q.group - 1);
-    const bool live = t < q.T;
-    float dot[KM];
-#pragma unroll
-    for (int j = 0; j < KM; ++j) dot[j] = 0.0f;
-    if (live) {
-        int row[KM];
-        float s[KM];
-        load_pairs<KM>(q, t, row, s);
-        const int chunks = (int)(q.H / VE);
-        const Tok *at = a + t * a_stride;
-        constexpr int U = kDot ? pair_unroll(VE, KM) : 4;
-        for (int c0 = local; c0 < chunks; c0 += U * q.group) {
-            // every load of the step before its first use
-            Chunk<Tok, VE> v[U];
-            Chunk<Row, VE> y[kDot ? U : 1][kDot ? KM : 1];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int c = c0 + u * q.group;
-                if (c >= chunks) continue;
-                v[u].load(at + (int64_t)c * VE);
-                if constexpr (kDot) {
-#pragma unroll
-                    for (int j = 0; j < KM; ++j)
-                        if (row[j] >= 0) y[u][j].load(src + row[j] * src_stride + (int64_t)c * VE);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int c = c0 + u * q.group;
-                if (c >= chunks) continue;
-#pragma unroll
-                for (int j = 0; j < KM; ++j) {
-                    if (row[j] < 0) continue;
-                    Chunk<Row, VE> o;
-#pragma unroll
-                    for (int i = 0; i < VE; ++i) {
-                        const float x = v[u].get(i);
-                        if constexpr (kDot) dot[j] = fmaf(x, y[u][j].get(i), dot[j]);
-                        o.set(i, x * s[j]);
-                    }
-                    o.store(rows + row[j] * rows_stride + (int64_t)c * VE);
-                }
-            }
-        }
-    }
-    if constexpr (kDot) write_dots<KM>(q, t, live, dot);
-}
-
-template <class Tok, class Row, int VE, int KM, bool kDot>
-__global__ void __launch_bounds__(kPairThreads, pair_blocks(KM)) sum_rows_kernel(PairRows q, const Row *__restrict__ rows,
-                                                                int64_t rows_stride, const Tok *__restrict__ a,
-                                                                int64_t a_stride, Tok *__restrict__ out,
-                                                                int64_t out_stride) {
-    pdl_wait();
-    pdl_trigger();
-    const int64_t t = (int64_t)blockIdx.x * (kPairThreads / q.group) + threadIdx.x / q.group;
-    const int local = threadIdx.x & (q.group - 1);
-    const bool live = t < q.T;
-    float dot[KM];
-#pragma unroll
-    for (int j = 0; j < KM; ++j) dot[j] = 0.0f;
-    if (live) {
-        int row[KM];
-        float s[KM];
-        load_pairs<KM>(q, t, row, s);
-        const int chunks = (int)(q.H / VE);
-        constexpr int U = pair_unroll(VE, KM);
-        for (int c0 = local; c0 < chunks; c0 += U * q.group) {
-            Chunk<Row, VE> y[U][KM];
-            Chunk<Tok, VE> x[kDot ? U : 1];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int c = c0 + u * q.group;
-                if (c >= chunks) continue;
-#pragma unroll
-                for (int j = 0; j < KM; ++j)
-                    if (row[j] >= 0) y[u][j].load(rows + row[j] * rows_stride + (int64_t)c * VE);
-                if constexpr (kDot) x[u].load(a + t * a_stride + (int64_t)c * VE);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int c = c0 + u * q.group;
-                if (c >= chunks) continue;
-                float acc[VE];
-#pragma unroll
-                for (int i = 0; i < VE; ++i) acc[i] = 0.0f;
-#pragma unroll
-                for (int j = 0; j < KM; ++j) {
-                    if (row[j] < 0) continue;
-#pragma unroll
-                    for (int i = 0; i < VE; ++i) {
-                        const float y_i = y[u][j].get(i);
-                        if constexpr (kDot) dot[j] = fmaf(x[u].get(i), y_i, dot[j]);
-                        acc[i] = fmaf(s[j], y_i, acc[i]);
-                    }
-                }
-                Chunk<Tok, VE> o;
-#pragma unroll
-                for (int i = 0; i < VE; ++i) o.set(i, acc[i]);
-                o.store(out + t * out_stride + (int64_t)c * VE);
-            }
-        }
-    }
-    if constexpr (kDot) write_dots<KM>(q, t, live, dot);
-}
-
-// ---- rows of 16-byte words --------------------------------------------------------------
 constexpr int kBulkWarps = 4;                          // computing warps; one more issues the copies
 constexpr int kBulkThreads = 32 * (kBulkWarps + 1);
 constexpr int kBulkStages = 4;
 
-// The operands; a stage holds `seg` elements of the token's row (a, if it is read) and of
-// each of its k expert rows (rows_in, if they are read).
+// The operands, strides in elements; a stage holds `seg` elements of the token's row (a, if
+// it is read) and of each of its k expert rows (rows_in, if they are read).
 struct PairBulk {
     const void *a, *rows_in;
     void *out;                    // sum: [T, H] of the token type; spread: [R, H] of the row type
     int64_t a_stride, rows_stride, out_stride;
-    int seg, stages, stage_bytes;
+    int seg, stages;
+    int a_slot, row_slot, stage_bytes;      // room for the token's row, an expert row, all of them
 };
 
-template <class Tok, class Row, int KM, bool kSum, bool kDot>
+// Lane j < k of a warp: the expert row of pair j of token t (-1: dropped) and its weight.
+// A row past the R rows of the buffer is dropped too and flagged.
+__device__ __forceinline__ void load_pair(const PairRows &q, int64_t t, int lane, int &r, float &w) {
+    r = -1;
+    w = 1.0f;
+    if (t >= q.T || lane >= q.k) return;
+    const int64_t p = t * q.k + lane, row = q.pair_rows ? (int64_t)__ldg(q.pair_rows + p) : p;
+    if (q.weights) w = __ldg(q.weights + p);
+    if (row >= q.R)
+        raise_device_error(MOE_DEVERR_OUT_OF_BOUNDS);
+    else
+        r = row < 0 ? -1 : (int)row;
+}
+
+// The 16-byte granules of [p, p + n * sizeof(T)) inside the tensor [base, end): what a bulk
+// copy brings (`lo`, `bytes`); elements in a granule that is not wholly the tensor's are
+// stored to `dst` (the shared address of the first granule) by this thread.
+template <class T>
+__device__ __forceinline__ void granules(const T *p, int n, const T *base, const T *end, uint8_t *dst, uintptr_t &lo,
+                                         uint32_t &bytes) {
+    const uintptr_t first = reinterpret_cast<uintptr_t>(p), last = reinterpret_cast<uintptr_t>(p + n);
+    const uintptr_t start = first & ~uintptr_t(15);
+    uintptr_t hi = (last + 15) & ~uintptr_t(15);
+    lo = start;
+    const auto plain = [&](uintptr_t from, uintptr_t to) {
+        for (uintptr_t i = from; i < to; i += sizeof(T))
+            *reinterpret_cast<T *>(dst + (i - start)) = *reinterpret_cast<const T *>(i);
+    };
+    if (lo < reinterpret_cast<uintptr_t>(base)) {
+        lo += 16;
+        plain(first, min(lo, last));
+    }
+    if (hi > reinterpret_cast<uintptr_t>(end) && hi > lo) {
+        hi -= 16;
+        plain(max(hi, max(first, lo)), last);
+    }
+    bytes = hi > lo ? (uint32_t)(hi - lo) : 0u;
+}
+
+// kWords: every row and segment of every operand lies on 16-byte words.
+template <class Tok, class Row, int KM, bool kSum, bool kDot, bool kWords>
 __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_constant__ PairRows q,
                                                                  const __grid_constant__ PairBulk b) {
     constexpr bool kReadsA = !kSum || kDot, kReadsRows = kSum || kDot;
@@ -297,29 +161,18 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
         if (!ptx::mbar_wait(a, parity)) *reinterpret_cast<volatile int *>(&failed) = 1;
     };
     const int H = (int)q.H, segs = (H + b.seg - 1) / b.seg;
-    const int a_bytes = kReadsA ? b.seg * (int)sizeof(Tok) : 0, row_bytes = b.seg * (int)sizeof(Row);
     int stage = 0;
     uint32_t phase = 0;
 
     if (warp == kBulkWarps) {
-        // lane j < k: pair j of the token, read one token ahead
-        const auto pair = [&](int64_t t, int &r, float &w) {
-            r = -1;
-            w = 1.0f;
-            if (t >= q.T || lane >= q.k) return;
-            const int64_t p = t * q.k + lane, row = q.pair_rows ? (int64_t)__ldg(q.pair_rows + p) : p;
-            if (q.weights) w = __ldg(q.weights + p);
-            if (row >= q.R)
-                raise_device_error(MOE_DEVERR_OUT_OF_BOUNDS);
-            else
-                r = row < 0 ? -1 : (int)row;
-        };
+        // lane j < k: the row of pair j, read one token ahead; lane 8: the token's row
+        const Tok *const a0 = static_cast<const Tok *>(b.a), *const a1 = a0 + (q.T - 1) * b.a_stride + q.H;
+        const Row *const r0 = static_cast<const Row *>(b.rows_in), *const r1 = r0 + (q.R - 1) * b.rows_stride + q.H;
         int r, next_r;
         float w, next_w;
-        pair(blockIdx.x, r, w);
+        load_pair(q, blockIdx.x, lane, r, w);
         for (int64_t t = blockIdx.x; t < q.T; t += gridDim.x) {
-            pair(t + gridDim.x, next_r, next_w);
-            const int used = __popc(__ballot_sync(0xFFFFFFFFu, r >= 0));
+            load_pair(q, t + gridDim.x, lane, next_r, next_w);
             for (int s = 0; s < segs; ++s) {
                 const int h0 = s * b.seg, n = min(b.seg, H - h0);
                 wait(empty[stage], phase ^ 1u);
@@ -328,17 +181,34 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
                     row_s[stage][lane] = r;
                     weight_s[stage][lane] = w;
                 }
+                uint8_t *dst = ring + stage * b.stage_bytes;
+                uintptr_t src = 0;
+                uint32_t bytes = 0;
+                if (kReadsRows && r >= 0) {
+                    dst += b.a_slot + lane * b.row_slot;
+                    const Row *p = r0 + r * b.rows_stride + h0;
+                    if constexpr (kWords) {
+                        src = reinterpret_cast<uintptr_t>(p);
+                        bytes = n * (int)sizeof(Row);
+                    } else {
+                        granules(p, n, r0, r1, dst, src, bytes);
+                        dst += src - (reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15));
+                    }
+                } else if (kReadsA && lane == 8) {
+                    const Tok *p = a0 + t * b.a_stride + h0;
+                    if constexpr (kWords) {
+                        src = reinterpret_cast<uintptr_t>(p);
+                        bytes = n * (int)sizeof(Tok);
+                    } else {
+                        granules(p, n, a0, a1, dst, src, bytes);
+                        dst += src - (reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15));
+                    }
+                }
+                const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, bytes), bar = ptx::smem_u32(&full[stage]);
+                __syncwarp();           // the plain stores above come before the arrival
+                if (lane == 0) ptx::mbar_arrive_expect_tx(bar, total);
                 __syncwarp();
-                const uint32_t bar = ptx::smem_u32(&full[stage]), dst = ptx::smem_u32(ring + stage * b.stage_bytes);
-                if (lane == 0)
-                    ptx::mbar_arrive_expect_tx(bar, (kReadsRows ? used * n * (int)sizeof(Row) : 0) +
-                                                        (kReadsA ? n * (int)sizeof(Tok) : 0));
-                __syncwarp();
-                if (kReadsRows && r >= 0)
-                    ptx::bulk_load(dst + a_bytes + lane * row_bytes,
-                                   static_cast<const Row *>(b.rows_in) + r * b.rows_stride + h0, n * (int)sizeof(Row), bar);
-                if (kReadsA && lane == 8)
-                    ptx::bulk_load(dst, static_cast<const Tok *>(b.a) + t * b.a_stride + h0, n * (int)sizeof(Tok), bar);
+                if (bytes) ptx::bulk_load(ptx::smem_u32(dst), reinterpret_cast<const void *>(src), bytes, bar);
                 if (++stage == b.stages) {
                     stage = 0;
                     phase ^= 1u;
@@ -358,27 +228,36 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
         for (int s = 0; s < segs; ++s) {
             const int h0 = s * b.seg, n = min(b.seg, H - h0);
             wait(full[stage], phase);
-            const uint8_t *sa = ring + stage * b.stage_bytes, *sr = sa + a_bytes;
+            const uint8_t *sa = ring + stage * b.stage_bytes;
             int row[KM];
             float w[KM];
+            const Row *y_s[KM];
 #pragma unroll
             for (int j = 0; j < KM; ++j) {
                 row[j] = row_s[stage][j];
                 w[j] = weight_s[stage][j];
+                const uint8_t *at = sa + b.a_slot + j * b.row_slot;
+                if (!kWords && kReadsRows)
+                    at += reinterpret_cast<uintptr_t>(static_cast<const Row *>(b.rows_in) + row[j] * b.rows_stride + h0) & 15u;
+                y_s[j] = reinterpret_cast<const Row *>(at);
             }
-            for (int c = tid * 8; c < n; c += 32 * kBulkWarps * 8) {
-                Chunk<Tok, 8> x, o;
-                if constexpr (kReadsA) x.load_shared(reinterpret_cast<const Tok *>(sa) + c);
-                float acc[8];
+            if (!kWords && kReadsA) sa += reinterpret_cast<uintptr_t>(static_cast<const Tok *>(b.a) + t * b.a_stride + h0) & 15u;
+            const Tok *x_s = reinterpret_cast<const Tok *>(sa);
+            constexpr int VE = kWords ? 8 : 1;
+#pragma unroll(kWords ? 1 : 2)
+            for (int c = tid * VE; c < n; c += 32 * kBulkWarps * VE) {
+                Chunk<Tok, VE> x, o;
+                if constexpr (kReadsA) x.load(x_s + c);
+                float acc[VE];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+                for (int i = 0; i < VE; ++i) acc[i] = 0.0f;
 #pragma unroll
                 for (int j = 0; j < KM; ++j) {
                     if (row[j] < 0) continue;
-                    Chunk<Row, 8> y, z;
-                    if constexpr (kReadsRows) y.load_shared(reinterpret_cast<const Row *>(sr + j * row_bytes) + c);
+                    Chunk<Row, VE> y, z;
+                    if constexpr (kReadsRows) y.load(y_s[j] + c);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < VE; ++i) {
                         if constexpr (kDot) dot[j] = fmaf(x.get(i), y.get(i), dot[j]);
                         if constexpr (kSum) acc[i] = fmaf(w[j], y.get(i), acc[i]);
                         if constexpr (!kSum) z.set(i, x.get(i) * w[j]);
@@ -387,7 +266,7 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
                 }
                 if constexpr (kSum) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o.set(i, acc[i]);
+                    for (int i = 0; i < VE; ++i) o.set(i, acc[i]);
                     o.store(static_cast<Tok *>(b.out) + t * b.out_stride + h0 + c);
                 }
             }
@@ -419,6 +298,69 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
     if (failed) {                 // a wait gave up: the copies still under way, once more with a limit
         for (int i = 0; i < b.stages; ++i) ptx::mbar_wait(ptx::smem_u32(&full[i]), i < stage ? phase : phase ^ 1u);
     }
+}
+
+// The spread of unweighted rows of one type, on 16-byte words: rows[r(p)] = a[t] bit for bit,
+// so nothing but copies.  One warp a block: a bulk copy brings a segment of a token's row
+// to shared memory, lanes j < k each send it on to their expert row.
+constexpr int kCopyStages = 4;
+
+__global__ void __launch_bounds__(32) copy_rows_kernel(const __grid_constant__ PairRows q, const __grid_constant__ PairBulk b,
+                                                       int elem) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ uint64_t full[kCopyStages];
+    const int lane = threadIdx.x, segs = (int)((q.H + b.seg - 1) / b.seg);
+    if (lane == 0) {
+        for (int i = 0; i < kCopyStages; ++i) ptx::mbar_init(ptx::smem_u32(&full[i]), 1);
+        ptx::fence_mbarrier_init();
+    }
+    __syncwarp();
+    pdl_wait();
+    pdl_trigger();
+    // the next segment to fetch (lane 0), and its stage
+    int64_t ft = blockIdx.x;
+    int fs = 0, fstage = 0;
+    const auto bytes_of = [&](int seg) { return (uint32_t)(min(b.seg, (int)q.H - seg * b.seg) * elem); };
+    const auto fetch = [&]() {
+        if (ft >= q.T) return;
+        const uint32_t bar = ptx::smem_u32(&full[fstage]), bytes = bytes_of(fs);
+        ptx::mbar_arrive_expect_tx(bar, bytes);
+        ptx::bulk_load(ptx::smem_u32(ring + fstage * b.stage_bytes),
+                       static_cast<const uint8_t *>(b.a) + (ft * b.a_stride + (int64_t)fs * b.seg) * elem, bytes, bar);
+        fstage = (fstage + 1) % kCopyStages;
+        if (++fs == segs) {
+            fs = 0;
+            ft += gridDim.x;
+        }
+    };
+    if (lane == 0)
+        for (int i = 0; i < kCopyStages - 1; ++i) fetch();
+    int r, next_r, stage = 0;
+    uint32_t phase = 0;
+    float w;
+    bool ok = true;
+    load_pair(q, blockIdx.x, lane, r, w);
+    for (int64_t t = blockIdx.x; t < q.T && ok; t += gridDim.x, r = next_r) {
+        load_pair(q, t + gridDim.x, lane, next_r, w);
+        for (int s = 0; s < segs && ok; ++s) {
+            ok = __all_sync(0xFFFFFFFFu, ptx::mbar_wait(ptx::smem_u32(&full[stage]), phase));
+            if (ok && r >= 0)
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                                 static_cast<uint8_t *>(b.out) + (r * b.out_stride + (int64_t)s * b.seg) * elem),
+                             "r"(ptx::smem_u32(ring + stage * b.stage_bytes)), "r"(bytes_of(s))
+                             : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            // the next fetch takes the previous segment's stage: that one is read when one group is left
+            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            __syncwarp();
+            if (lane == 0 && ok) fetch();
+            stage = (stage + 1) % kCopyStages;
+            if (stage == 0) phase ^= 1u;
+        }
+    }
+    if (!ok)                      // a wait gave up (flagged): the copies still under way, once more with a limit
+        for (int i = 0; i < kCopyStages; ++i) ptx::mbar_wait(ptx::smem_u32(&full[i]), i < stage ? phase : phase ^ 1u);
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 }  // namespace moe
