@@ -68,7 +68,6 @@ struct Tile {
 // 1024-byte boundary).
 struct Layout {
     int nt;                // rows of x per tile, at most kTok
-    int rows;              // weight rows of an item
     int stages;            // of the weight ring, which starts at 0
     int scale_bufs;        // items whose scales are held
     int scale_stride;      // of a weight row's scales
@@ -331,22 +330,18 @@ __device__ __forceinline__ int stage_x(const Params &q, Shared &sh, uint8_t *xs,
     return ntok;
 }
 
-// What an item needs besides codes: the scale bytes of weight rows n0 .. n0 + rows - 1 of
-// expert e, their bias (fp32, 0 without one) and scale2 (gate, up) behind them.  The scales
-// are a run of bytes that starts anywhere, copied as the 16-byte granules that hold it (the
-// first byte lands at its address modulo 16); where rows of a multiple of 32 bytes would
-// put the same bytes of many rows into one bank, a copy per row spreads them.  Called by
-// one warp; arrives once on `full`.
-template <bool kNv, bool kSwiGlu>
+// The scale bytes of weight rows n0 .. n0 + rows - 1 of expert e.  They are a run of bytes
+// that starts anywhere, copied as the 16-byte granules that hold it (the first byte lands
+// at its address modulo 16); where rows of a multiple of 32 bytes would put the same bytes
+// of many rows into one bank, a copy per row spreads them.  Called by one warp; arrives
+// once on `full`, behind all that the warp has written.
+template <bool kNv>
 __device__ __forceinline__ void issue_scales(const Params &q, uint8_t *dst, uint64_t &full, int e, int n0, int rows) {
     const int per_row = q.K / (kNv ? 16 : 32), lane = threadIdx.x & 31;
     const uint32_t bar = ptx::smem_u32(&full);
     const int64_t row0 = (int64_t)e * q.N + n0, first = row0 * per_row, last = first + (int64_t)rows * per_row;
-    float *tail = reinterpret_cast<float *>(dst + q.L.scale_bytes) - 2;
-    if (q.bias)
-        for (int r = lane; r < rows; r += 32) tail[r - q.L.rows] = __ldg(q.bias + row0 + r);
-    if (kNv && lane < 2) tail[lane] = q.scale2 ? __ldg(q.scale2 + (kSwiGlu ? 2 * e + lane : e)) : 1.0f;
     if (q.L.scale_stride != per_row) {
+        __syncwarp();
         if (lane == 0) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(rows * per_row));
         __syncwarp();
         for (int r = lane; r < rows; r += 32)
@@ -499,39 +494,62 @@ __global__ void __launch_bounds__(T::kThreads, 1) matvec_kernel(const __grid_con
     uint32_t phase = 0, sphase = 0;
 
     if (warp == T::kWarps) {
-        for (int it = beg; it < end; ++it) {
+        // The bias and scale2 of an item are loaded while the item before it is issued: waiting
+        // for plain loads here would hold the weights up.
+        float bias[T::kRows / 32] = {}, scale2 = 1.0f;
+        const auto load_tail = [&]() {
+            const int64_t row = (int64_t)e * q.N + tile * T::kRows + lane;
+#pragma unroll
+            for (int i = 0; i < T::kRows / 32; ++i)
+                if (q.bias && tile * T::kRows + lane + 32 * i < q.N) bias[i] = __ldg(q.bias + row + 32 * i);
+            if (kNv && q.scale2 && lane < 2) scale2 = __ldg(q.scale2 + (kSwiGlu ? 2 * e + lane : e));
+        };
+        const auto find_expert = [&]() {
             while (sh.start[e + 1] <= slot) ++e;
-            const int n0 = tile * T::kRows;
+        };
+        if (beg < end) {
+            find_expert();
+            load_tail();
+        }
+        for (int it = beg; it < end; ++it) {
+            const int e0 = e, n0 = tile * T::kRows;
             for (int c = 0; c < chunks; ++c) {
                 wait_or_fail(sh, sh.empty[stage], phase ^ 1u);
                 __syncwarp();
                 if (lane == 0) {
                     const uint32_t bar = ptx::smem_u32(&sh.full[stage]);
-                    const int units = min(T::kStageK, q.K - c * T::kStageK);
-                    const int boxes = (units + 255) / 256;
+                    const int boxes = (min(T::kStageK, q.K - c * T::kStageK) + 255) / 256;
                     ptx::mbar_arrive_expect_tx(bar, boxes * T::kBoxBytes);
                     for (int b = 0; b < boxes; ++b)
                         ptx::tma_load_2d(ptx::smem_u32(sm + stage * T::kStageBytes + b * T::kBoxBytes), &weights,
-                                         c * (T::kStageK / 2) + b * 128, e * q.N + n0, bar);
-                }
-                if (c == 0) {
-                    wait_or_fail(sh, sh.scales_empty[sbuf], sphase ^ 1u);
-                    __syncwarp();
-                    issue_scales<kNv, kSwiGlu>(q, sm + q.L.scales + sbuf * q.L.scale_bytes, sh.scales_full[sbuf], e, n0,
-                                      min(T::kRows, q.N - n0));
-                    if (++sbuf == q.L.scale_bufs) {
-                        sbuf = 0;
-                        sphase ^= 1u;
-                    }
+                                         c * (T::kStageK / 2) + b * 128, e0 * q.N + n0, bar);
                 }
                 if (++stage == q.L.stages) {
                     stage = 0;
                     phase ^= 1u;
                 }
-            }
-            if (++tile == n_tiles) {
-                tile = 0;
-                ++slot;
+                if (c == 0) {
+                    wait_or_fail(sh, sh.scales_empty[sbuf], sphase ^ 1u);
+                    __syncwarp();
+                    uint8_t *dst = sm + q.L.scales + sbuf * q.L.scale_bytes;
+                    float *tail = reinterpret_cast<float *>(dst + q.L.scale_bytes) - 2;
+#pragma unroll
+                    for (int i = 0; i < T::kRows / 32; ++i) tail[lane + 32 * i - T::kRows] = bias[i];
+                    if (lane < 2) tail[lane] = scale2;
+                    issue_scales<kNv>(q, dst, sh.scales_full[sbuf], e0, n0, min(T::kRows, q.N - n0));
+                    if (++sbuf == q.L.scale_bufs) {
+                        sbuf = 0;
+                        sphase ^= 1u;
+                    }
+                    if (++tile == n_tiles) {
+                        tile = 0;
+                        ++slot;
+                    }
+                    if (it + 1 < end) {
+                        find_expert();
+                        load_tail();
+                    }
+                }
             }
         }
         return;
@@ -635,7 +653,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) matvec_kernel(const __grid_con
             for (int w = 0; w < T::kSplit; ++w) v += red[w * kRed + o];
             const bool live = n < q.N && tok < ntok;
             if constexpr (kNv) v = live ? scale_pow2(v, sh.tok_exp[tok]) * tail[kSwiGlu ? row & 1 : 0] : 0.0f;
-            if (q.bias) v += tail[row - T::kRows];
+            v += tail[row - T::kRows];
             if constexpr (kSwiGlu) {
                 const float up = __shfl_xor_sync(0xFFFFFFFFu, v, kTok);      // row + 1
                 if (live && !(row & 1))

@@ -814,7 +814,6 @@ moe::mv::Layout matvec_layout(int64_t R, int64_t K, int block, int limit) {
     namespace mv = moe::mv;
     mv::Layout L{};
     L.xs = mv::x_row_stride((int)K);
-    L.rows = T::kRows;
     L.scale_stride = (int)(K / block);
     if (L.scale_stride % 32 == 0) L.scale_stride += 16;
     L.scale_bytes = (T::kRows * (L.scale_stride + 4) + 8 + 15 + 127) / 128 * 128;
