@@ -94,12 +94,15 @@ struct Params {
 // 16-byte loads fall into different banks.
 __host__ __device__ constexpr int x_row_stride(int K) { return 2 * K + ((64 - 2 * K) & 127); }
 
-// Clamped SwiGLU with the library exponential and a full division: the result may be kept
-// in fp32.
-__device__ __forceinline__ float clamped_swiglu_f32(float gate, float up, float alpha, float limit) {
-    const float g = fminf(gate, limit);
-    const float u = fminf(fmaxf(up, -limit), limit);
-    return (u + 1.0f) * (g / (1.0f + expf(-alpha * g)));
+// Clamped SwiGLU; a NaN stays one (fminf would replace it by the limit).  A result kept in
+// fp32 gets the library exponential and a full division; the fast forms' 1e-6 is far below
+// the rounding of a 16-bit one.
+template <class Out>
+__device__ __forceinline__ float swiglu(float gate, float up, float alpha, float limit) {
+    const float g = gate > limit ? limit : gate;
+    const float u = up > limit ? limit : up < -limit ? -limit : up;
+    const float sig = sizeof(Out) == 4 ? 1.0f / (1.0f + expf(-alpha * g)) : __fdividef(1.0f, 1.0f + __expf(-alpha * g));
+    return (u + 1.0f) * (g * sig);
 }
 
 // Eight E2M1 codes (element 2j in the low nibble of byte j) -> four f16x2 words.
@@ -643,25 +646,22 @@ __global__ void __launch_bounds__(T::kThreads, 1) matvec_kernel(const __grid_con
         }
         group_barrier(group, 32 * T::kSplit);
         const float *tail = reinterpret_cast<const float *>(sm + q.L.scales + (sbuf + 1) * q.L.scale_bytes) - 2;
-#pragma unroll
-        for (int j = 0; j < (kRed + 32 * T::kSplit - 1) / (32 * T::kSplit); ++j) {
-            const int o = (j * T::kSplit + part) * 32 + lane;
-            if (o >= kRed) break;                                      // whole warps
-            const int row = group * T::kGroupRows + o / kTok, tok = o % kTok, n = tile * T::kRows + row;
+        const auto joined = [&](int row, int tok) {      // row of the group
             float v = 0.0f;
 #pragma unroll
-            for (int w = 0; w < T::kSplit; ++w) v += red[w * kRed + o];
-            const bool live = n < q.N && tok < ntok;
-            if constexpr (kNv) v = live ? scale_pow2(v, sh.tok_exp[tok]) * tail[kSwiGlu ? row & 1 : 0] : 0.0f;
-            v += tail[row - T::kRows];
-            if constexpr (kSwiGlu) {
-                const float up = __shfl_xor_sync(0xFFFFFFFFu, v, kTok);      // row + 1
-                if (live && !(row & 1))
-                    static_cast<Out *>(q.out)[(int64_t)sh.tok_row[tok] * n_out + n / 2] =
-                        f32_to_elem<Out>(clamped_swiglu_f32(v, up, q.alpha, q.limit));
-            } else if (live) {
-                static_cast<Out *>(q.out)[(int64_t)sh.tok_row[tok] * n_out + n] = f32_to_elem<Out>(v);
-            }
+            for (int w = 0; w < T::kSplit; ++w) v += red[w * kRed + row * kTok + tok];
+            if constexpr (kNv) v = scale_pow2(v, tok < ntok ? sh.tok_exp[tok] : 0) * tail[kSwiGlu ? row & 1 : 0];
+            return v + tail[group * T::kGroupRows + row - T::kRows];
+        };
+        // a thread's output: a row and a column, or a gate and up row (2i, 2i + 1) and a column
+        constexpr int kOutputs = kSwiGlu ? kRed / 2 : kRed;
+#pragma unroll
+        for (int j = 0; j < (kOutputs + 32 * T::kSplit - 1) / (32 * T::kSplit); ++j) {
+            const int o = (j * T::kSplit + part) * 32 + lane, tok = o % kTok, row = (kSwiGlu ? 2 : 1) * (o / kTok);
+            if (o >= kOutputs || n0 + row >= q.N || tok >= ntok) continue;
+            float v = joined(row, tok);
+            if constexpr (kSwiGlu) v = swiglu<Out>(v, joined(row + 1, tok), q.alpha, q.limit);
+            static_cast<Out *>(q.out)[(int64_t)sh.tok_row[tok] * n_out + (n0 + row) / (kSwiGlu ? 2 : 1)] = f32_to_elem<Out>(v);
         }
         __syncwarp();
         if (lane == 0) {

@@ -214,6 +214,49 @@ def test_infinities_and_nan_in_x(moe_gpu, fmt):
     assert moe.moe_get_device_error() == 0
 
 
+@pytest.mark.parametrize("odt", ["bfloat16", "float32"])
+def test_infinities_and_nan_through_the_activation(moe_gpu, odt):
+    # NaN stays NaN in the gate and in the up output (an invalid scale among the causes); an infinite
+    # gate or up output is clamped like any large one
+    import torch
+    moe = moe_gpu
+    K, N = 64, 8
+    blocks = np.zeros((N, K // 2), np.uint8)
+    blocks[:, 0] = 0x02                                                     # W[n, 0] = 1, the rest 0
+    blocks[0, :] = 0x00
+    blocks[2:4, 16] = 0x02                                                  # outputs 2, 3 also read x[32]
+    blocks[5, 16] = 0x02                                                    # output 5 (an up) does
+    blocks[6, 16] = 0x02                                                    # output 6 (a gate) does
+    scales = np.full((N, K // 32), 127, np.uint8)
+    x = torch.zeros((4, K), dtype=torch.bfloat16)
+    x[:, 0] = 1.0
+    x[1, 32], x[2, 32], x[3, 0] = float("inf"), 1.0, 0.0
+    gu = x.double().numpy()[:, [0]].repeat(N, axis=1)
+    gu[:, 0] = 0
+    bad = scales.copy()
+    bad[6, 1] = 255
+    got = moe.mxfp4_matvec(x.cuda(), _dev(blocks), _dev(scales), swiglu=True, out_dtype=getattr(torch, odt)).double().cpu().numpy()
+    y = gu.copy()
+    for n in (2, 3, 5, 6):
+        y[:, n] += x.double().numpy()[:, 32]
+    # every output reads 0 * x[32] too: row 1's infinity makes those NaN
+    y[1, [0, 1, 4, 7]] = np.nan
+    with np.errstate(invalid="ignore"):
+        g = np.where(y[:, ::2] > LIMIT, LIMIT, y[:, ::2])
+        u = np.where(y[:, 1::2] > LIMIT, LIMIT, y[:, 1::2])
+        want = (u + 1) * g / (1 + np.exp(-ALPHA * g))
+    np.testing.assert_array_equal(np.isnan(got), np.isnan(want))
+    ok = ~np.isnan(want)
+    # products and sums here are exact: 32 roundings of the activation, one of the result
+    u_ = torch.finfo(getattr(torch, odt)).eps / 2
+    assert (np.abs(got[ok] - want[ok]) <= (u_ + 32 * 2.0 ** -24) * np.abs(want[ok])).all()
+    assert np.isnan(want).any() and np.isfinite(want[1]).any()
+    moe.moe_get_device_error()
+    got = moe.mxfp4_matvec(x.cuda(), _dev(blocks), _dev(bad), swiglu=True, out_dtype=getattr(torch, odt)).cpu()
+    assert moe.moe_get_device_error() == moe.MOE_DEVERR_BAD_SCALE
+    assert bool(torch.isnan(got[:, 3]).all()) and bool(torch.isfinite(got[0, :3]).all())
+
+
 @pytest.mark.parametrize("fmt,bad", [("mxfp4", 255), ("nvfp4", 0x7F), ("nvfp4", 0xFF)])
 def test_an_invalid_scale_is_nan_and_flagged(moe_gpu, fmt, bad):
     import torch
