@@ -427,16 +427,18 @@ int moe_route_backward(const float *dweights, const int32_t *ids, const float *w
  * Sums in fp32, one rounding.  A row whose id falls outside [0, E) is left unwritten and
  * raises MOE_DEVERR_BAD_EXPERT_ID; an invalid scale byte that is read makes its outputs
  * NaN and raises MOE_DEVERR_BAD_SCALE.  bf16 values below 2^-31 of the largest finite one
- * of their row of x count to within 2^-39 of that.  Meant for decode, where each weight
+ * of their row of x count to within 2^-39 of that, and an E8M0 block scaled 2^127 or more
+ * below another of its row may count as 0.  Meant for decode, where each weight
  * byte serves few rows and HBM bounds the product: weights are read once for every 8
  * rows of an expert.  Sizes: 1 <= R <= MOE_MATVEC_MAX_ROWS; 1 <= E <= 256; N <= 2^24;
- * K <= 2^16 (beyond: MOE_ERR_UNSUPPORTED); K % 32 == 0; N even with
+ * K <= MOE_MATVEC_MAX_K; E * N < 2^31 (beyond: MOE_ERR_UNSUPPORTED); K % 32 == 0; N even with
  * MOE_FLAG_SWIGLU.  x, blocks and scales 16-byte aligned, x_stride a multiple of 8.
  * Errors: MOE_ERR_INVALID_ARG for null pointers, sizes, alignment, flags;
  * MOE_ERR_UNSUPPORTED for types.
  */
 #define MOE_FLAG_SWIGLU 0x2u
 #define MOE_MATVEC_MAX_ROWS 1024
+#define MOE_MATVEC_MAX_K 32768
 int mxfp4_matvec(const void *x, int x_dtype, int64_t x_stride, int rows_per_x, int64_t R, int64_t N,
                  int64_t K, int64_t E, const int32_t *row_ids, const uint8_t *blocks,
                  const uint8_t *scales, const float *bias, uint32_t flags, float alpha, float limit,

@@ -11,6 +11,7 @@
 #include <initializer_list>
 #include <map>
 #include <mutex>
+#include <new>
 #include <tuple>
 #include <type_traits>
 #include <utility>
@@ -291,9 +292,12 @@ bool ensure_smem_attr(const void *kernel, int bytes) {
         return false;
     }
     if (ctx != 0) {
-        std::lock_guard<std::mutex> lock(mu);
-        int &v = done[key];
-        if (v < bytes) v = bytes;
+        try {
+            std::lock_guard<std::mutex> lock(mu);
+            int &v = done[key];
+            if (v < bytes) v = bytes;
+        } catch (const std::bad_alloc &) {      // not remembered: set again by the next call
+        }
     }
     return true;
 }
@@ -872,10 +876,12 @@ int launch_matvec_tile(moe::mv::Params q, const uint8_t *blocks, int optin, cuda
 // What a call costs with tile T, in weight rows of one SM at the rate of the tallest tile:
 // rounds of items over the SMs times an item's rows over the tile's rate.  A taller tile
 // spreads its bookkeeping over more rows, a lower one leaves fewer SMs idle in the last
-// round.  Rates measured on 1 GB of weights (gate_up of 64 tokens over 128 experts, us):
-// 128 rows 192, 64 rows 222, 32 rows 337.  The estimate picks the fastest of the three at
-// each size measured: one row of 2880 x 2880 9.2 / 7.2 / 6.3 us, one token's four experts
-// 18.3 / 16.3 / 18.5, eight tokens' down products 27.5 / 28.0 / 36.9.
+// round.  Rates measured on 0.98 GB of weights (gate_up of 64 tokens over 128 experts): 128
+// rows 186 us, 64 rows 206, 32 rows 300.  The estimate picks the fastest of the three, or one
+// within 3% of it, at each size measured (128 / 64 / 32 rows): one row of 2880 x 2880 9.5 / 7.2 /
+// 6.2 us, one token's four experts 17.7 / 15.4 / 16.7, eight tokens' down products 28.2 / 27.4 /
+// 33.3, one row of 8192 x 8192 21.5 / 13.6 / 15.9; eight rows of 28672 x 8192, which only the low
+// tile leaves room for at once, 76.5 / 73.6 / 50.3.
 template <class T>
 double matvec_cost(const moe::mv::Params &q, int block, int optin, double rate) {
     const moe::mv::Layout L = matvec_layout<T>(q.R, q.K, block, optin);
@@ -890,10 +896,10 @@ int launch_matvec(const moe::mv::Params &q, const uint8_t *blocks, cudaStream_t 
     using Middle = moe::mv::Tile<16, 8, 2, 4>;    // 64 x 1024
     using Low = moe::mv::Tile<16, 16, 2, 2>;      // 32 x 1024
     const int optin = max_smem_optin(), block = kNv ? 16 : 32;
-    const double tall = matvec_cost<Tall>(q, block, optin, 1.0), middle = matvec_cost<Middle>(q, block, optin, 0.87),
-                 low = matvec_cost<Low>(q, block, optin, 0.57);
-    if (tall <= middle && tall <= low && tall < 1e30) return launch_matvec_tile<Tall, X, Out, kNv, kSwiGlu>(q, blocks, optin, s);
-    if (middle <= low && middle < 1e30) return launch_matvec_tile<Middle, X, Out, kNv, kSwiGlu>(q, blocks, optin, s);
+    const double tall = matvec_cost<Tall>(q, block, optin, 1.0), middle = matvec_cost<Middle>(q, block, optin, 0.90),
+                 low = matvec_cost<Low>(q, block, optin, 0.62);
+    if (tall <= middle && tall <= low) return launch_matvec_tile<Tall, X, Out, kNv, kSwiGlu>(q, blocks, optin, s);
+    if (middle <= low) return launch_matvec_tile<Middle, X, Out, kNv, kSwiGlu>(q, blocks, optin, s);
     return launch_matvec_tile<Low, X, Out, kNv, kSwiGlu>(q, blocks, optin, s);
 }
 
@@ -908,7 +914,7 @@ int matvec(const void *x, int x_dtype, int64_t x_stride, int rows_per_x, int64_t
         (swiglu && N % 2 != 0))
         return MOE_ERR_INVALID_ARG;
     if (!dtype_size(x_dtype) || !dtype_size(out_dtype)) return MOE_ERR_INVALID_ARG;
-    if (R > MOE_MATVEC_MAX_ROWS || E > moe::mv::kMaxExperts || N > (1 << 24) || K > (1 << 16) || E * N >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    if (R > MOE_MATVEC_MAX_ROWS || E > moe::mv::kMaxExperts || N > (1 << 24) || K > MOE_MATVEC_MAX_K || E * N >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
     if (x_dtype == MOE_DTYPE_F32 || (out_dtype != x_dtype && out_dtype != MOE_DTYPE_F32)) return MOE_ERR_UNSUPPORTED;
     if (!aligned(x, 16) || (x_stride % 8) != 0 || !aligned(blocks, 16) || !aligned(scales, 16) || !aligned(row_ids, 4) ||
         !aligned(scale2, 4) || !aligned(bias, 4) || !aligned(out, dtype_size(out_dtype)))

@@ -20,6 +20,13 @@
 // memory, not of registers and warps.  Rows that do not lie on 16-byte words come as the
 // 16-byte granules that hold them and are taken apart element by element; the granules at
 // the two ends of a tensor, which may not be its own, are read with plain loads.
+//
+// Measured (device time; share of the 6.55 TB/s copy rate): combine's gradient with the dots,
+// 8192 tokens x 4 x 2880 bf16, 76 us, 86%; combine, 4096 x 4 x 2880 bf16, 21 us, 84%; dispatch's
+// gradient with the dots, same sizes, 26 us, 84%; combine of fp32 rows 35 us, 93%; 4096 x 4 rows
+// of 1001 bf16 11 us, 57%.  With direct loads (four 16-byte ones in flight a thread) these took
+// 85, 23, 32, 35 and 18 us.  The spread without dots writes four times what it reads: 45 us
+// at 8192 tokens, 80%, by copies and by stores alike.
 #pragma once
 #include <cuda_fp16.h>
 

@@ -87,6 +87,7 @@ SHAPES = [
     (64, 4, 128, 32, 1024, True),
     (5, 3, 200, 18, 8192, True),        # long K, many experts
     (1, 1, 1, 6, 20000, False),
+    (5, 1, 1, 70, 32768, False),        # the longest rows: fewer rows of x at a time
 ]
 
 

@@ -96,7 +96,7 @@ MATVEC_CHANGES = [
     (dict(flags=2, N=33), INVALID), (dict(x=P + 8), INVALID), (dict(blocks=P + 8), INVALID), (dict(scales=P + 4), INVALID),
     (dict(x_stride=68), INVALID), (dict(x_stride=-64), INVALID), (dict(bias=P + 2), INVALID), (dict(row_ids=P + 1), INVALID),
     (dict(out=P + 1), INVALID), (dict(x_dtype=5), INVALID), (dict(out_dtype=9), INVALID),
-    (dict(R=1025), UNSUPPORTED), (dict(E=257), UNSUPPORTED), (dict(N=2 ** 24 + 1), UNSUPPORTED), (dict(K=2 ** 24 + 32), UNSUPPORTED),
+    (dict(R=1025), UNSUPPORTED), (dict(E=257), UNSUPPORTED), (dict(N=2 ** 24 + 1), UNSUPPORTED), (dict(K=2 ** 15 + 32), UNSUPPORTED), (dict(N=2 ** 24, E=128), UNSUPPORTED),
     (dict(x_dtype=F32), UNSUPPORTED), (dict(out_dtype=F16), UNSUPPORTED)]
 
 
