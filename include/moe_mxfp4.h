@@ -378,7 +378,7 @@ typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 } moe_dt
  * moe_permute's are; the others may name a row twice.  Products and sums are fp32 in a
  * fixed order, every result is rounded once; outputs must not alias inputs.
  * Types: rows_dtype equal to the token side's type, or MOE_DTYPE_F32 (else
- * MOE_ERR_UNSUPPORTED).  Sizes: T, H, R >= 1; 1 <= k <= 8; T*k, R, H < 2^31; pointers
+ * MOE_ERR_UNSUPPORTED).  Sizes: T, H, R >= 1; 1 <= k <= 8; T*k, R < 2^31; H <= 2^30; pointers
  * aligned to their elements (16-byte aligned rows and strides and H % 8 == 0 are the
  * fast case).  Errors: MOE_ERR_INVALID_ARG for null pointers, sizes, strides, alignment.
  */

@@ -531,6 +531,7 @@ def moe_dispatch_rows(x, pair_rows, k: int, weights=None, n_rows: Optional[int] 
     say otherwise); rows that no pair names are left as they were."""
     c = _Call(x, stream)
     T, H = x.shape
+    k = int(k)
     if rows is None:
         rows = c.empty(x, (T * k if n_rows is None else n_rows, H), dtype or x.dtype)
     R = rows.shape[0]
@@ -551,6 +552,7 @@ def moe_dispatch_rows_backward(drows, pair_rows, T: int, k: int, weights=None, x
     Returns dx, or (dx, dweights)."""
     c = _Call(drows, stream)
     R, H = drows.shape
+    T, k = int(T), int(k)
     if dx is None:
         dx = c.empty(drows, (T, H), dtype or (drows.dtype if x is None else x.dtype))
     if x is None:
@@ -576,6 +578,7 @@ def moe_combine_rows(rows, pair_rows, T: int, k: int, weights=None, dtype=None, 
     default; fp32 rows may go to bf16 or fp16)."""
     c = _Call(rows, stream)
     R, H = rows.shape
+    T, k = int(T), int(k)
     if out is None:
         out = c.empty(rows, (T, H), dtype or rows.dtype)
     rp, rd, rs = c.rows(rows, "rows", R, H)
@@ -597,6 +600,7 @@ def moe_combine_rows_backward(dout, pair_rows, k: int, weights=None, y_rows=None
     were.  Returns drows, or (drows, dweights)."""
     c = _Call(dout, stream)
     T, H = dout.shape
+    k = int(k)
     if drows is None:
         n = y_rows.shape[0] if y_rows is not None else T * k if n_rows is None else n_rows
         drows = c.empty(dout, (n, H), dtype or (dout.dtype if y_rows is None else y_rows.dtype))
@@ -622,6 +626,7 @@ def moe_route_backward(dweights, ids, weights, E: int, dlogits=None, stream=None
     returned -> fp32 dlogits [T, E], zero for the experts that were not chosen."""
     c = _Call(dweights, stream)
     T, k = dweights.shape
+    E = int(E)
     if dlogits is None:
         dlogits = c.empty(dweights, (T, E), _t.float32)
     f32 = _t.float32
@@ -637,6 +642,7 @@ def _matvec(name, block, x, blocks, scales, scale2, bias, row_ids, rows_per_x, s
             stream):
     c = _Call(x, stream)
     Tx, K = x.shape
+    rows_per_x = int(rows_per_x)
     E, N, Kh = blocks.shape if blocks.dim() == 3 else (1, *blocks.shape)
     if Kh * 2 != K:
         raise ValueError(f"{name}: x has {K} columns, the weights {2 * Kh}")

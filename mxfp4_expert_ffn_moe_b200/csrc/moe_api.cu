@@ -697,7 +697,7 @@ bool rows_of_words(int64_t H, std::initializer_list<RowsArg> rows) {
 
 bool pair_sizes_ok(int64_t T, int64_t H, int k, int64_t R) {
     return T >= 1 && H >= 1 && k >= 1 && k <= 8 && R >= 1 && T * k < (int64_t(1) << 31) && R < (int64_t(1) << 31) &&
-           H < (int64_t(1) << 31);
+           H <= (int64_t(1) << 30);
 }
 
 // Shared memory: stages of at most 32 KB (the row split into equal segments, multiples of 8

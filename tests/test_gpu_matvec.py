@@ -88,6 +88,9 @@ SHAPES = [
     (5, 3, 200, 18, 8192, True),        # long K, many experts
     (1, 1, 1, 6, 20000, False),
     (5, 1, 1, 70, 32768, False),        # the longest rows: fewer rows of x at a time
+    (8, 1, 1, 8190, 512, False),        # items of 64 weight rows, one partial stage
+    (16, 4, 4, 1500, 2912, True),       # items of 128, up to two tiles of x per expert, a ragged last stage
+    (16, 4, 16, 1500, 640, True),
 ]
 
 

@@ -89,7 +89,9 @@ SHAPES = [
     (300, 4, 32, 2880, 0.05),
     (19, 5, 9, 40, 0.5),            # more slots than 4, few chunks
     (5000, 2, 4, 64, 0.0),          # a warp per token
-    (6, 7, 8, 8200, 0.0),           # long rows
+    (6, 7, 8, 8200, 0.0),           # long rows, in segments
+    (7, 8, 8, 8201, 0.2),           # the same off 16-byte words
+    (700, 8, 16, 24, 0.1),
 ]
 
 
@@ -297,6 +299,29 @@ def test_the_same_call_gives_the_same_bits_on_any_stream_and_in_a_graph(moe_gpu)
     assert all(torch.equal(a, b) for a, b in zip(captured, want))
 
 
+def test_the_bounds_checked_build_gives_the_same(moe_gpu):
+    import torch
+    from mxfp4_expert_ffn_moe_b200 import build as moe_build
+    moe_build.build(checked=True)
+    moe = moe_gpu
+    T, k, H = 90, 3, 250
+    pair_rows, w, R, g = _case(T, k, 8, H, 0.1, seed=21)
+    x, y = _randn((T, H), "float16", g), _randn((R, H), "float16", g)
+    results = []
+    for checked in (False, True):
+        moe.use_checked_library(checked)
+        try:
+            moe.moe_get_device_error()
+            rows = moe.moe_dispatch_rows(x, pair_rows, k, weights=w, n_rows=R)
+            results.append((rows, moe.moe_combine_rows(y, pair_rows, T, k, weights=w),
+                            *moe.moe_combine_rows_backward(x, pair_rows, k, weights=w, y_rows=y),
+                            *moe.moe_dispatch_rows_backward(y, pair_rows, T, k, weights=w, x=x)))
+            assert moe.moe_get_device_error() == 0
+        finally:
+            moe.use_checked_library(False)
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
 # ---- the router's gradient -----------------------------------------------------------
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 4, 2), (37, 7, 7), (300, 32, 4), (65, 200, 8), (5, 255, 8),
                                    (513, 256, 8), (4096, 32, 4), (2, 3, 1)])
@@ -317,6 +342,21 @@ def test_route_backward_against_64_bits(moe_gpu, T, E, k):
     chosen = torch.zeros((T, E), dtype=torch.bool, device="cuda").scatter_(1, ids.long(), True)
     assert bool((got[~chosen] == 0).all())
     assert moe.moe_get_device_error() == 0
+
+
+def test_route_backward_into_an_unaligned_gradient(moe_gpu):
+    import torch
+    moe = moe_gpu
+    T, E, k = 301, 32, 4
+    g = torch.Generator().manual_seed(9)
+    ids, w = moe.moe_route(torch.randn((T, E), generator=g).cuda(), k)
+    dw = torch.randn((T, k), generator=g).cuda()
+    want = moe.moe_route_backward(dw, ids, w, E)
+    for off in (1, 2, 3):
+        buf = torch.full((T * E + 8,), 5.0, device="cuda")
+        got = moe.moe_route_backward(dw, ids, w, E, dlogits=buf[off:off + T * E].view(T, E))
+        assert torch.equal(got, want)
+        assert bool((buf[:off] == 5).all()) and bool((buf[off + T * E:] == 5).all())
 
 
 def test_route_backward_against_differences(moe_gpu):
