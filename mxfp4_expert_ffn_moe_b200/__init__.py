@@ -490,10 +490,11 @@ class _Call:
             self.stream = stream.cuda_stream
 
     def empty(self, like, shape, dtype):
+        # (empty_strided takes 1.5 us where new_empty takes 1.9 and empty 2.3)
         if self.side is None:
-            return like.new_empty(shape, dtype=dtype)
+            return _t.empty_strided(shape, (shape[1], 1), dtype=dtype, device=like.device)
         with _t.cuda.stream(self.side):
-            return like.new_empty(shape, dtype=dtype)
+            return _t.empty_strided(shape, (shape[1], 1), dtype=dtype, device=like.device)
 
     def flat(self, t, dtype, name, numel):
         """Contiguous tensor of `numel` elements (None stays None)."""
