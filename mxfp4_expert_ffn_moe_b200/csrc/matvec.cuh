@@ -203,18 +203,9 @@ struct Shared {
     int tok_row[kTok];              // rows r of the staged tile
     int tok_exp[kTok];              // x = staged value * 2^tok_exp
     unsigned tok_max[kTok];
-    int failed;                     // a wait gave up: all later waits return at once
+    int failed;                     // a wait gave up
     int16_t ids[kMaxRows];          // the rows' experts, -1 outside [0, E)
 };
-
-__device__ __noinline__ void slow_wait(Shared &sh, uint32_t bar, uint32_t parity) {
-    volatile int *failed = &sh.failed;
-    if (!*failed && !ptx::mbar_wait(bar, parity)) *failed = 1;
-}
-__device__ __forceinline__ void wait_or_fail(Shared &sh, uint64_t &bar, uint32_t parity) {
-    const uint32_t a = ptx::smem_u32(&bar);
-    if (!ptx::mbar_test_wait(a, parity)) slow_wait(sh, a, parity);
-}
 
 // Rows per expert and the first tile of each.  Called by the whole block.
 template <class T>
@@ -522,11 +513,12 @@ __global__ void __launch_bounds__(T::kThreads, 1) matvec_kernel(const __grid_con
             find_expert();
             load_tail();
         }
-        for (int it = beg; it < end; ++it) {
+        bool ok = true;
+        for (int it = beg; it < end && ok; ++it) {
             const int e0 = e, n0 = tile * T::kRows;
             for (int c = 0; c < chunks; ++c) {
-                wait_or_fail(sh, sh.empty[stage], phase ^ 1u);
-                __syncwarp();
+                ok = __all_sync(0xFFFFFFFFu, wait_or_fail(sh.failed, sh.empty[stage], phase ^ 1u));
+                if (!ok) break;
                 if (lane == 0) {
                     const uint32_t bar = ptx::smem_u32(&sh.full[stage]);
                     const int boxes = (min(T::kStageK, q.K - c * T::kStageK) + 255) / 256;
@@ -540,8 +532,8 @@ __global__ void __launch_bounds__(T::kThreads, 1) matvec_kernel(const __grid_con
                     phase ^= 1u;
                 }
                 if (c == 0) {
-                    wait_or_fail(sh, sh.scales_empty[sbuf], sphase ^ 1u);
-                    __syncwarp();
+                    ok = __all_sync(0xFFFFFFFFu, wait_or_fail(sh.failed, sh.scales_empty[sbuf], sphase ^ 1u));
+                    if (!ok) break;
                     uint8_t *dst = sm + q.L.scales + sbuf * q.L.scale_bytes;
                     float *tail = reinterpret_cast<float *>(dst + q.L.scale_bytes) - 2;
 #pragma unroll
@@ -562,6 +554,11 @@ __global__ void __launch_bounds__(T::kThreads, 1) matvec_kernel(const __grid_con
                     }
                 }
             }
+        }
+        if (!ok) {                // the copies still under way, waited for with a limit
+            for (int i = 0; i < q.L.stages; ++i) ptx::mbar_wait(ptx::smem_u32(&sh.full[i]), i < stage ? phase : phase ^ 1u);
+            for (int i = 0; i < q.L.scale_bufs; ++i)
+                ptx::mbar_wait(ptx::smem_u32(&sh.scales_full[i]), i < sbuf ? sphase : sphase ^ 1u);
         }
         return;
     }
@@ -593,7 +590,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) matvec_kernel(const __grid_con
         rs.ref = -1;
         rs.bytes = ptx::smem_u32(sm + q.L.scales) + sbuf * q.L.scale_bytes +
                    ((uint32_t)(e * q.N + tile * T::kRows) * (uint32_t)per_row & 15u) + my_row * q.L.scale_stride;
-        wait_or_fail(sh, sh.scales_full[sbuf], sphase);
+        wait_or_fail(sh.failed, sh.scales_full[sbuf], sphase);
         float acc[T::kTiles][4];
 #pragma unroll
         for (int m = 0; m < T::kTiles; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.0f;
@@ -601,7 +598,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) matvec_kernel(const __grid_con
             const int first = c * (T::kStageK / 32) + part;
             const int n = (q.K / 32 - first + T::kSplit - 1) / T::kSplit;        // at least kBlocks in a whole stage
             if (n > 0) make_factors<T, kNv>(factors, rs, first, n, acc);
-            wait_or_fail(sh, sh.full[stage], phase);
+            wait_or_fail(sh.failed, sh.full[stage], phase);
             const uint32_t w = ring + stage * T::kStageBytes, x = x0 + c * (T::kStageK * 2);
             if (n >= T::kBlocks)
                 multiply_blocks<T, kNv, true>(w, unit, x, factors, n, acc);
@@ -646,7 +643,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) matvec_kernel(const __grid_con
         // join the warps' sums, in warp order; then scale2, bias, activation, one rounding
         float *red = reinterpret_cast<float *>(sm + q.L.red) + group * T::kSplit * kRed;
         float *mine = red + part * kRed + g * kTok + 2 * t;
-        wait_or_fail(sh, sh.red_empty[group], ((it - beg) & 1) ^ 1u);      // the previous item's are read
+        wait_or_fail(sh.failed, sh.red_empty[group], ((it - beg) & 1) ^ 1u);      // the previous item's are read
 #pragma unroll
         for (int m = 0; m < T::kTiles; ++m) {
             *reinterpret_cast<float2 *>(mine + 16 * m * kTok) = make_float2(acc[m][0], acc[m][1]);
@@ -684,11 +681,6 @@ __global__ void __launch_bounds__(T::kThreads, 1) matvec_kernel(const __grid_con
             tile = 0;
             ++slot;
         }
-    }
-    if (sh.failed) {                 // a wait gave up: the copies still under way, once more with a limit
-        for (int i = 0; i < q.L.stages; ++i) ptx::mbar_wait(ptx::smem_u32(&sh.full[i]), i < stage ? phase : phase ^ 1u);
-        for (int i = 0; i < q.L.scale_bufs; ++i)
-            ptx::mbar_wait(ptx::smem_u32(&sh.scales_full[i]), i < sbuf ? sphase : sphase ^ 1u);
     }
 }
 

@@ -77,6 +77,18 @@ struct Chunk {
     }
 };
 
+// Wait of a block that shares the flag `failed`: false once a wait gave up (and raised the
+// device error).  Then the others return at once, nothing more is fetched, and the loops
+// run out over what the buffers hold.
+__device__ __forceinline__ bool wait_or_fail(int &failed, uint64_t &bar, uint32_t parity) {
+    const uint32_t a = ptx::smem_u32(&bar);
+    volatile int *flag = &failed;
+    if (ptx::mbar_test_wait(a, parity)) return true;
+    if (!*flag && ptx::mbar_wait(a, parity)) return true;
+    *flag = 1;
+    return false;
+}
+
 // What the kernels take.
 struct PairRows {
     int64_t T, H, R;
@@ -151,6 +163,7 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
     __shared__ float part[2][kBulkWarps][KM];
     __shared__ int failed;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid < kBulkStages * 8) row_s[tid / 8][tid % 8] = -1;      // at all times a row of the buffer or none
     if (tid == 0) {
         for (int i = 0; i < b.stages; ++i) {
             ptx::mbar_init(ptx::smem_u32(&full[i]), 1);
@@ -162,11 +175,7 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
     __syncthreads();
     pdl_wait();
     pdl_trigger();
-    const auto wait = [&](uint64_t &bar, uint32_t parity) {      // after one wait gave up, none waits again
-        const uint32_t a = ptx::smem_u32(&bar);
-        if (ptx::mbar_test_wait(a, parity) || *reinterpret_cast<volatile int *>(&failed)) return;
-        if (!ptx::mbar_wait(a, parity)) *reinterpret_cast<volatile int *>(&failed) = 1;
-    };
+    const auto wait = [&](uint64_t &bar, uint32_t parity) { return wait_or_fail(failed, bar, parity); };
     const int H = (int)q.H, segs = (H + b.seg - 1) / b.seg;
     int stage = 0;
     uint32_t phase = 0;
@@ -178,12 +187,13 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
         int r, next_r;
         float w, next_w;
         load_pair(q, blockIdx.x, lane, r, w);
-        for (int64_t t = blockIdx.x; t < q.T; t += gridDim.x) {
+        bool ok = true;
+        for (int64_t t = blockIdx.x; t < q.T && ok; t += gridDim.x) {
             load_pair(q, t + gridDim.x, lane, next_r, next_w);
             for (int s = 0; s < segs; ++s) {
                 const int h0 = s * b.seg, n = min(b.seg, H - h0);
-                wait(empty[stage], phase ^ 1u);
-                __syncwarp();
+                ok = __all_sync(0xFFFFFFFFu, wait(empty[stage], phase ^ 1u));
+                if (!ok) break;
                 if (lane < 8) {
                     row_s[stage][lane] = r;
                     weight_s[stage][lane] = w;
@@ -224,6 +234,8 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
             r = next_r;
             w = next_w;
         }
+        if (!ok)                  // the copies still under way, waited for with a limit
+            for (int i = 0; i < b.stages; ++i) ptx::mbar_wait(ptx::smem_u32(&full[i]), i < stage ? phase : phase ^ 1u);
         return;
     }
 
@@ -301,9 +313,6 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
                 q.dots[t * q.k + tid] = v;
             }
         }
-    }
-    if (failed) {                 // a wait gave up: the copies still under way, once more with a limit
-        for (int i = 0; i < b.stages; ++i) ptx::mbar_wait(ptx::smem_u32(&full[i]), i < stage ? phase : phase ^ 1u);
     }
 }
 
