@@ -32,11 +32,12 @@
 // 32 elements of every stage; their sums are joined in warp order, so the same call gives
 // the same bits.
 //
-// Measured (device time, gate_up of 64 tokens over 128 experts of 5760 x 2880, 0.98 GB): 186 us,
-// 5.3 TB/s, 81% of the copy rate; 150 us with the arithmetic left out.  No single part holds
-// it back (without the decode 180, without the mma 195, without the factors 182, without
-// the join 179): sixteen warps' dependent steps per stage do.  Under the power cap of a
-// long run (1.7 GHz) it takes 215 us.  More warps with fewer registers, eight warps with
+// Measured (device time, gate_up of 64 tokens over 128 experts of 5760 x 2880, 0.98 GB): 184 us,
+// 5.3 TB/s, 82% of the copy rate; 150 us with the products left out, and 185 us with all
+// weights in L2, so the computing warps bound it.  No single part holds them back (of 193 us
+// then: without the decode 180, the mma 195, the factors 182, the join 179): sixteen warps'
+// dependent steps per stage do.  Under the power cap of a long run (1.7 GHz) it takes 215 to
+// 220 us.  More warps with fewer registers, eight warps with
 // twice the rows, epilogue warps of their own, deeper or shallower rings and factors made a
 // stage ahead were all slower.
 #pragma once
@@ -154,8 +155,9 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Loads of shared memory keep their order with the barriers around them, but may move past
-// arithmetic.
+// Loads of shared memory are volatile: they keep their order with the barriers around them,
+// but may move past arithmetic.
+
 // Four 8-row x 16-byte matrices, a row address from each lane (lane l: row l % 8 of matrix
 // l / 8): lane (g, t) receives word t of row g of each.
 __device__ __forceinline__ uint4 ldmatrix4(uint32_t a) {
