@@ -75,10 +75,14 @@ Workspace workspace_layout(int64_t T, int64_t H, int64_t I, int64_t E, int k) {
     return w;
 }
 
+// Whether T * k pairs fit the kernels' 32-bit row indices (k >= 1; the product itself may
+// pass 64 bits).
+bool pairs_fit(int64_t T, int k) { return T <= ((int64_t(1) << 31) - 1) / k; }
+
 bool forward_sizes_ok(int64_t T, int64_t H, int64_t I, int64_t E, int k) {
     if (T < 1 || E < 1 || E > 256 || k < 1 || k > 8 || k > E) return false;
     if (H < 64 || I < 64 || H % 64 != 0 || I % 64 != 0) return false;
-    if (T * k >= (int64_t(1) << 31)) return false;
+    if (!pairs_fit(T, k)) return false;
     if (2 * I >= (int64_t(1) << 31) || H >= (int64_t(1) << 31)) return false;
     return true;
 }
@@ -696,7 +700,7 @@ bool rows_of_words(int64_t H, std::initializer_list<RowsArg> rows) {
 }
 
 bool pair_sizes_ok(int64_t T, int64_t H, int k, int64_t R) {
-    return T >= 1 && H >= 1 && k >= 1 && k <= 8 && R >= 1 && T * k < (int64_t(1) << 31) && R < (int64_t(1) << 31) &&
+    return T >= 1 && H >= 1 && k >= 1 && k <= 8 && R >= 1 && pairs_fit(T, k) && R < (int64_t(1) << 31) &&
            H <= (int64_t(1) << 30);
 }
 
@@ -1066,7 +1070,7 @@ int moe_gather_pairs(const uint16_t *x, int64_t T, int64_t H, int k, const int32
     if (!x || !ids || !weights || !sorted_pairs || !offsets || !x_rows || !row_ids || !row_weights)
         return MOE_ERR_INVALID_ARG;
     if (T < 1 || k < 1 || k > 8 || E < 1 || E > 256 || H < 8 || H % 8 != 0) return MOE_ERR_INVALID_ARG;
-    if (T * k >= (int64_t(1) << 31)) return MOE_ERR_INVALID_ARG;
+    if (!pairs_fit(T, k)) return MOE_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(x_rows, 16)) return MOE_ERR_INVALID_ARG;
     const int64_t P = T * k;
     const int64_t grid = moe::ceil_div(P, 8) < sm_count() * 8 ? moe::ceil_div(P, 8) : sm_count() * 8;
@@ -1143,7 +1147,7 @@ int moe_route_backward(const float *dweights, const int32_t *ids, const float *w
                        float *dlogits, void *stream) {
     NvtxRange nvtx("moe_route_backward");
     if (!dweights || !ids || !weights || !dlogits) return MOE_ERR_INVALID_ARG;
-    if (T < 1 || E < 1 || k < 1 || k > 8 || k > E || T * k >= (int64_t(1) << 31)) return MOE_ERR_INVALID_ARG;
+    if (T < 1 || E < 1 || k < 1 || k > 8 || k > E || !pairs_fit(T, k)) return MOE_ERR_INVALID_ARG;
     if (E > 256) return MOE_ERR_UNSUPPORTED;
     if (!aligned(dweights, 4) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(dlogits, 4))
         return MOE_ERR_INVALID_ARG;
@@ -1177,7 +1181,7 @@ int moe_permute(const int32_t *ids, int64_t T, int k, int64_t E, int tile_rows, 
     NvtxRange nvtx("moe_permute");
     if (!ids || !counts || !offsets || !tile_offsets || !sorted_pairs) return MOE_ERR_INVALID_ARG;
     if (T < 1 || k < 1 || k > 8 || E < 1 || E > 256 || tile_rows < 1) return MOE_ERR_INVALID_ARG;
-    if (T * k >= (int64_t(1) << 31)) return MOE_ERR_INVALID_ARG;
+    if (!pairs_fit(T, k)) return MOE_ERR_INVALID_ARG;
     return launch_permute(ids, 0, T * k, E, tile_rows, counts, offsets, tile_offsets, sorted_pairs, pair_rows,
                           (cudaStream_t)stream);
 }

@@ -1,0 +1,30 @@
+"""Sizes at the ends of their types.  No GPU: the host-side checks run before any CUDA call."""
+import pytest
+
+import mxfp4_expert_ffn_moe_b200 as moe
+from mxfp4_expert_ffn_moe_b200 import build as moe_build
+
+P = 0x1000                                     # an address that is never used
+INVALID = -1
+BF16, F32 = 0, 2
+
+
+@pytest.fixture(scope="module")
+def lib():
+    moe_build.build()
+    return moe.load_library()
+
+
+@pytest.mark.parametrize("T,k", [(2 ** 61, 8), (2 ** 62, 4), (2 ** 63 - 1, 2), (2 ** 31, 1), (2 ** 28, 8),
+                                 ((2 ** 31 - 1) // 3 + 1, 3)])
+def test_a_number_of_pairs_past_32_or_64_bits_is_refused(lib, T, k):
+    # T * k of the first three is 0 or negative in 64 bits
+    assert lib.moe_dispatch_rows(P, BF16, 64, T, 64, k, P, P, 16, P, BF16, 64, None) == INVALID
+    assert lib.moe_dispatch_rows_backward(P, F32, 64, T, 64, k, 16, P, P, P, 64, P, F32, 64, P, None) == INVALID
+    assert lib.moe_combine_rows(P, F32, 64, T, 64, k, 16, P, P, P, BF16, 64, None) == INVALID
+    assert lib.moe_combine_rows_backward(P, BF16, 64, T, 64, k, P, P, P, 64, 16, P, BF16, 64, P, None) == INVALID
+    assert lib.moe_route_backward(P, P, P, T, 16, k, P, None) == INVALID
+    assert lib.moe_permute(P, T, k, 16, 32, P, P, P, P, None, None) == INVALID
+    assert lib.moe_gather_pairs(P, T, 64, k, P, P, P, P, 16, P, P, P, None) == INVALID
+    assert lib.moe_mxfp4_workspace_size(T, 128, 128, 16, k) == 0
+    assert lib.moe_token_tile_rows(T, 128, 128, 16, k, 0) == INVALID
