@@ -46,6 +46,7 @@
 #include "common.cuh"
 #include "dequant.cuh"
 #include "pair_rows.cuh"
+#include "ring.cuh"
 #include "sm100_ptx.cuh"
 
 namespace moe {
@@ -557,11 +558,8 @@ __global__ void __launch_bounds__(T::kThreads, 1) matvec_kernel(const __grid_con
                 }
             }
         }
-        if (!ok) {                // the copies still under way, waited for with a limit
-            for (int i = 0; i < q.L.stages; ++i) ptx::mbar_wait(ptx::smem_u32(&sh.full[i]), i < stage ? phase : phase ^ 1u);
-            for (int i = 0; i < q.L.scale_bufs; ++i)
-                ptx::mbar_wait(ptx::smem_u32(&sh.scales_full[i]), i < sbuf ? sphase : sphase ^ 1u);
-        }
+        wait_for_fills(sh.full, q.L.stages, stage, phase);
+        wait_for_fills(sh.scales_full, q.L.scale_bufs, sbuf, sphase);
         return;
     }
 
@@ -573,6 +571,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) matvec_kernel(const __grid_con
     const uint32_t unit = ((part ^ lane) & 7) << 4;
     const uint32_t factors = ptx::smem_u32(sm + q.L.factors) + warp * (kNv ? 2 : 1) * (T::kFactorBytes / T::kWarps);
     int staged = -1, ntok = 0;
+    bool ok = true;                                    // no wait of this thread for a copy gave up
     int tok_exp[2] = {0, 0};
     uint32_t x0 = 0;
     for (int it = beg; it < end; ++it) {
@@ -592,7 +591,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) matvec_kernel(const __grid_con
         rs.ref = -1;
         rs.bytes = ptx::smem_u32(sm + q.L.scales) + sbuf * q.L.scale_bytes +
                    ((uint32_t)(e * q.N + tile * T::kRows) * (uint32_t)per_row & 15u) + my_row * q.L.scale_stride;
-        wait_or_fail(sh.failed, sh.scales_full[sbuf], sphase);
+        ok = ok && wait_or_fail(sh.failed, sh.scales_full[sbuf], sphase);
         float acc[T::kTiles][4];
 #pragma unroll
         for (int m = 0; m < T::kTiles; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.0f;
@@ -600,14 +599,14 @@ __global__ void __launch_bounds__(T::kThreads, 1) matvec_kernel(const __grid_con
             const int first = c * (T::kStageK / 32) + part;
             const int n = (q.K / 32 - first + T::kSplit - 1) / T::kSplit;        // at least kBlocks in a whole stage
             if (n > 0) make_factors<T, kNv>(factors, rs, first, n, acc);
-            wait_or_fail(sh.failed, sh.full[stage], phase);
+            ok = ok && wait_or_fail(sh.failed, sh.full[stage], phase);
             const uint32_t w = ring + stage * T::kStageBytes, x = x0 + c * (T::kStageK * 2);
             if (n >= T::kBlocks)
                 multiply_blocks<T, kNv, true>(w, unit, x, factors, n, acc);
             else if (n > 0)
                 multiply_blocks<T, kNv, false>(w, unit, x, factors, n, acc);
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.empty[stage]));
+            if (lane == 0 && ok) ptx::mbar_arrive(ptx::smem_u32(&sh.empty[stage]));
             if (++stage == q.L.stages) {
                 stage = 0;
                 phase ^= 1u;
@@ -673,7 +672,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) matvec_kernel(const __grid_con
         __syncwarp();
         if (lane == 0) {
             ptx::mbar_arrive(ptx::smem_u32(&sh.red_empty[group]));
-            ptx::mbar_arrive(ptx::smem_u32(&sh.scales_empty[sbuf]));
+            if (ok) ptx::mbar_arrive(ptx::smem_u32(&sh.scales_empty[sbuf]));
         }
         if (++sbuf == q.L.scale_bufs) {
             sbuf = 0;

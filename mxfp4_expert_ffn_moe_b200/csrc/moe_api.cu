@@ -1266,6 +1266,14 @@ int moe_profile_read(double *ms, int64_t *launches) {
     return rc;
 }
 
+#if MOE_CHECKED
+// Bounds-checked builds only: whether the waits of the row and matvec kernels give up at once
+// (MOE_DEVERR_TIMEOUT; such a call's outputs mean nothing).
+int moe_checked_give_up_waits(int on) {
+    return cudaMemcpyToSymbol(moe::g_give_up_waits, &on, sizeof(int)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+#endif
+
 int moe_get_device_error(void *stream) {
     if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return MOE_ERR_CUDA;
     int v = 0;

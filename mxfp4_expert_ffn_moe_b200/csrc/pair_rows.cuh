@@ -31,6 +31,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "ring.cuh"
 #include "sm100_ptx.cuh"
 
 namespace moe {
@@ -76,18 +77,6 @@ struct Chunk {
         w[i / n].e[i % n] = f32_to_elem<T>(v);
     }
 };
-
-// Wait of a block that shares the flag `failed`: false once a wait gave up (and raised the
-// device error).  Then the others return at once, nothing more is fetched, and the loops
-// run out over what the buffers hold.
-__device__ __forceinline__ bool wait_or_fail(int &failed, uint64_t &bar, uint32_t parity) {
-    const uint32_t a = ptx::smem_u32(&bar);
-    volatile int *flag = &failed;
-    if (ptx::mbar_test_wait(a, parity)) return true;
-    if (!*flag && ptx::mbar_wait(a, parity)) return true;
-    *flag = 1;
-    return false;
-}
 
 // What the kernels take.
 struct PairRows {
@@ -175,7 +164,6 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
     __syncthreads();
     pdl_wait();
     pdl_trigger();
-    const auto wait = [&](uint64_t &bar, uint32_t parity) { return wait_or_fail(failed, bar, parity); };
     const int H = (int)q.H, segs = (H + b.seg - 1) / b.seg;
     int stage = 0;
     uint32_t phase = 0;
@@ -192,7 +180,7 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
             load_pair(q, t + gridDim.x, lane, next_r, next_w);
             for (int s = 0; s < segs; ++s) {
                 const int h0 = s * b.seg, n = min(b.seg, H - h0);
-                ok = __all_sync(0xFFFFFFFFu, wait(empty[stage], phase ^ 1u));
+                ok = __all_sync(0xFFFFFFFFu, wait_or_fail(failed, empty[stage], phase ^ 1u));
                 if (!ok) break;
                 if (lane < 8) {
                     row_s[stage][lane] = r;
@@ -234,19 +222,19 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
             r = next_r;
             w = next_w;
         }
-        if (!ok)                  // the copies still under way, waited for with a limit
-            for (int i = 0; i < b.stages; ++i) ptx::mbar_wait(ptx::smem_u32(&full[i]), i < stage ? phase : phase ^ 1u);
+        wait_for_fills(full, b.stages, stage, phase);
         return;
     }
 
     int turn = 0;
+    bool ok = true;                     // no wait of this thread gave up
     for (int64_t t = blockIdx.x; t < q.T; t += gridDim.x, turn ^= 1) {
         float dot[KM];
 #pragma unroll
         for (int j = 0; j < KM; ++j) dot[j] = 0.0f;
         for (int s = 0; s < segs; ++s) {
             const int h0 = s * b.seg, n = min(b.seg, H - h0);
-            wait(full[stage], phase);
+            ok = ok && wait_or_fail(failed, full[stage], phase);
             const uint8_t *sa = ring + stage * b.stage_bytes;
             int row[KM];
             float w[KM];
@@ -290,7 +278,7 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
                 }
             }
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&empty[stage]));
+            if (lane == 0 && ok) ptx::mbar_arrive(ptx::smem_u32(&empty[stage]));
             if (++stage == b.stages) {
                 stage = 0;
                 phase ^= 1u;
@@ -333,24 +321,27 @@ __global__ void __launch_bounds__(32) copy_rows_kernel(const __grid_constant__ P
     __syncwarp();
     pdl_wait();
     pdl_trigger();
-    // the next segment to fetch (lane 0), and its stage
+    // the next segment to fetch, its stage and that stage's parity; lane 0 issues the copy
     int64_t ft = blockIdx.x;
     int fs = 0, fstage = 0;
+    uint32_t fphase = 0;
     const auto bytes_of = [&](int seg) { return (uint32_t)(min(b.seg, (int)q.H - seg * b.seg) * elem); };
     const auto fetch = [&]() {
         if (ft >= q.T) return;
-        const uint32_t bar = ptx::smem_u32(&full[fstage]), bytes = bytes_of(fs);
-        ptx::mbar_arrive_expect_tx(bar, bytes);
-        ptx::bulk_load(ptx::smem_u32(ring + fstage * b.stage_bytes),
-                       static_cast<const uint8_t *>(b.a) + (ft * b.a_stride + (int64_t)fs * b.seg) * elem, bytes, bar);
+        if (lane == 0) {
+            const uint32_t bar = ptx::smem_u32(&full[fstage]), bytes = bytes_of(fs);
+            ptx::mbar_arrive_expect_tx(bar, bytes);
+            ptx::bulk_load(ptx::smem_u32(ring + fstage * b.stage_bytes),
+                           static_cast<const uint8_t *>(b.a) + (ft * b.a_stride + (int64_t)fs * b.seg) * elem, bytes, bar);
+        }
         fstage = (fstage + 1) % kCopyStages;
+        if (fstage == 0) fphase ^= 1u;
         if (++fs == segs) {
             fs = 0;
             ft += gridDim.x;
         }
     };
-    if (lane == 0)
-        for (int i = 0; i < kCopyStages - 1; ++i) fetch();
+    for (int i = 0; i < kCopyStages - 1; ++i) fetch();
     int r, next_r, stage = 0;
     uint32_t phase = 0;
     float w;
@@ -359,7 +350,7 @@ __global__ void __launch_bounds__(32) copy_rows_kernel(const __grid_constant__ P
     for (int64_t t = blockIdx.x; t < q.T && ok; t += gridDim.x, r = next_r) {
         load_pair(q, t + gridDim.x, lane, next_r, w);
         for (int s = 0; s < segs && ok; ++s) {
-            ok = __all_sync(0xFFFFFFFFu, ptx::mbar_wait(ptx::smem_u32(&full[stage]), phase));
+            ok = __all_sync(0xFFFFFFFFu, ring_wait(full[stage], phase));
             if (ok && r >= 0)
                 asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
                                  static_cast<uint8_t *>(b.out) + (r * b.out_stride + (int64_t)s * b.seg) * elem),
@@ -369,13 +360,12 @@ __global__ void __launch_bounds__(32) copy_rows_kernel(const __grid_constant__ P
             // the next fetch takes the previous segment's stage: that one is read when one group is left
             asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
             __syncwarp();
-            if (lane == 0 && ok) fetch();
+            if (ok) fetch();
             stage = (stage + 1) % kCopyStages;
             if (stage == 0) phase ^= 1u;
         }
     }
-    if (!ok)                      // a wait gave up (flagged): the copies still under way, once more with a limit
-        for (int i = 0; i < kCopyStages; ++i) ptx::mbar_wait(ptx::smem_u32(&full[i]), i < stage ? phase : phase ^ 1u);
+    if (!ok) wait_for_fills(full, kCopyStages, fstage, fphase);      // a wait gave up, up to three fetches behind the last
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
