@@ -359,6 +359,7 @@ __device__ __forceinline__ void issue_scales(const Params &q, uint8_t *dst, uint
         hi = total & ~int64_t(15);
         const int64_t i = max(hi, first) + lane;
         if (i < total) dst[i - lo] = __ldg(q.scales + i);
+        ptx::fence_proxy_async_smem();      // a later item's copy writes there through the async proxy
     }
     __syncwarp();
     if (lane == 0) {

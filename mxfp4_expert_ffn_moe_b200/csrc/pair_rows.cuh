@@ -117,7 +117,8 @@ __device__ __forceinline__ void load_pair(const PairRows &q, int64_t t, int lane
 
 // The 16-byte granules of [p, p + n * sizeof(T)) inside the tensor [base, end): what a bulk
 // copy brings (`lo`, `bytes`); elements in a granule that is not wholly the tensor's are
-// stored to `dst` (the shared address of the first granule) by this thread.
+// stored to `dst` (the shared address of the first granule) by this thread.  A later copy
+// into the same stage writes there through the async proxy, hence the fence.
 template <class T>
 __device__ __forceinline__ void granules(const T *p, int n, const T *base, const T *end, uint8_t *dst, uintptr_t &lo,
                                          uint32_t &bytes) {
@@ -128,6 +129,7 @@ __device__ __forceinline__ void granules(const T *p, int n, const T *base, const
     const auto plain = [&](uintptr_t from, uintptr_t to) {
         for (uintptr_t i = from; i < to; i += sizeof(T))
             *reinterpret_cast<T *>(dst + (i - start)) = *reinterpret_cast<const T *>(i);
+        ptx::fence_proxy_async_smem();
     };
     if (lo < reinterpret_cast<uintptr_t>(base)) {
         lo += 16;
