@@ -9,9 +9,6 @@
 
 #include <algorithm>
 #include <initializer_list>
-#include <map>
-#include <mutex>
-#include <new>
 #include <tuple>
 #include <type_traits>
 #include <utility>
@@ -29,6 +26,7 @@
 #include "dequant.cuh"
 #include "gemm_mxf.cuh"
 #include "gemm_swap.cuh"
+#include "largest_set.h"
 #include "matvec.cuh"
 #include "pair_rows.cuh"
 #include "permute.cuh"
@@ -280,30 +278,15 @@ bool make_packed_map(CUtensorMap *m, const void *ptr, int64_t E, int64_t N, int6
 // context; the largest size already set is remembered per (kernel, device, context), so
 // that repeated calls of an entry point skip it (a new context is a miss).
 bool ensure_smem_attr(const void *kernel, int bytes) {
-    static std::mutex mu;
-    static std::map<std::tuple<const void *, int, unsigned long long>, int> done;
+    static moe::LargestSet<std::tuple<const void *, int, unsigned long long>> set;
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
     const unsigned long long ctx = moe::current_context_id();
-    const auto key = std::make_tuple(kernel, dev, ctx);
-    if (ctx != 0) {
-        std::lock_guard<std::mutex> lock(mu);
-        const auto it = done.find(key);
-        if (it != done.end() && it->second >= bytes) return true;
-    }
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    return set.ensure(std::make_tuple(kernel, dev, ctx), bytes, ctx == 0, [&](int size) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, size) == cudaSuccess) return true;
         cudaGetLastError();
         return false;
-    }
-    if (ctx != 0) {
-        try {
-            std::lock_guard<std::mutex> lock(mu);
-            int &v = done[key];
-            if (v < bytes) v = bytes;
-        } catch (const std::bad_alloc &) {      // not remembered: set again by the next call
-        }
-    }
-    return true;
+    });
 }
 
 int max_smem_optin() {

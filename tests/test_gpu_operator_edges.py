@@ -45,3 +45,38 @@ def test_the_bank_s_last_scales_take_turns_with_others(moe_gpu):
     got = moe.mxfp4_matvec(_dev(x, torch.bfloat16), _dev(blocks), _dev(scales), row_ids=_dev(ids), out_dtype=torch.float32)
     want, _, _ = _want(x, _weights(blocks, scales, "mxfp4"), ids, 1, None, None, False)
     np.testing.assert_array_equal(got.double().cpu().numpy(), want)
+
+
+def test_two_host_threads_at_once(moe_gpu):
+    # one instantiation, a small and a large shared-memory size, from two threads on their own streams
+    import threading
+
+    import torch
+    moe = moe_gpu
+    g = torch.Generator().manual_seed(60)
+    T, k = 40, 7
+    cases, errors = [], []
+    for H in (8, 2880):
+        y, w = _randn((T * k, H), "float16", g), torch.rand((T, k), generator=g).cuda()
+        cases.append((y, w, (y.double().view(T, k, H) * w.double()[:, :, None]).sum(1)))
+    torch.cuda.synchronize()
+
+    def work(case):
+        y, w, want = case
+        stream = torch.cuda.Stream()
+        try:
+            for _ in range(50):
+                out = moe.moe_combine_rows(y, None, T, k, weights=w, stream=stream)
+            stream.synchronize()
+            # k fused steps of 2^-24 on sums below 2^6, and one rounding to fp16
+            assert bool(((out.double() - want).abs() <= 2.0 ** -11 * want.abs() + k * 2.0 ** -18).all())
+        except Exception as e:                                       # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(c,)) for c in cases for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    assert moe.moe_get_device_error() == 0
