@@ -347,6 +347,9 @@ int moe_combine_pairs(const float *y_rows, const int32_t *pair_rows, int64_t T, 
  * A decode step of a few tokens without a sort or a copy, rows in pair order:
  *   moe_route, mxfp4_matvec (gate_up, MOE_FLAG_SWIGLU, rows_per_x = k, row_ids = ids),
  *   mxfp4_matvec (down, fp32 out, row_ids = ids), moe_combine_rows (pair_rows NULL).
+ * Both products take MOE_FLAG_ZERO_SKIPPED there: a token with fewer than k non-NaN logits
+ * has slots with id -1 and weight 0 (moe_route), whose rows the products leave out and the
+ * combine multiplies by 0.
  */
 
 /* Element types of the calls below. */
@@ -424,8 +427,9 @@ int moe_route_backward(const float *dweights, const int32_t *ids, const float *w
  *   scale2   fp32 (nvfp4) [E], with MOE_FLAG_SWIGLU [E, 2] (gate, up), or NULL (= 1)
  *   bias     fp32 [E, N] or NULL;  alpha, limit: used with MOE_FLAG_SWIGLU only
  *   out      of out_dtype: x_dtype or MOE_DTYPE_F32
- * Sums in fp32, one rounding.  A row whose id falls outside [0, E) is left unwritten and
- * raises MOE_DEVERR_BAD_EXPERT_ID; an invalid scale byte that is read makes its outputs
+ * Sums in fp32, one rounding.  A row whose id falls outside [0, E) raises
+ * MOE_DEVERR_BAD_EXPERT_ID and is left unwritten, or with MOE_FLAG_ZERO_SKIPPED becomes a
+ * row of zeros; an invalid scale byte that is read makes its outputs
  * NaN and raises MOE_DEVERR_BAD_SCALE.  bf16 values below 2^-31 of the largest finite one
  * of their row of x count to within 2^-39 of that, and an E8M0 block scaled 2^127 or more
  * below another of its row may count as 0.  Meant for decode, where each weight
@@ -437,6 +441,7 @@ int moe_route_backward(const float *dweights, const int32_t *ids, const float *w
  * MOE_ERR_UNSUPPORTED for types.
  */
 #define MOE_FLAG_SWIGLU 0x2u
+#define MOE_FLAG_ZERO_SKIPPED 0x8u    /* rows that the call would leave as they were become zeros */
 #define MOE_MATVEC_MAX_ROWS 1024
 #define MOE_MATVEC_MAX_K 32768
 int mxfp4_matvec(const void *x, int x_dtype, int64_t x_stride, int rows_per_x, int64_t R, int64_t N,

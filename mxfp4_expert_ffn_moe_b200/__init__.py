@@ -26,6 +26,7 @@ __all__ = [
     "MOE_DEVERR_BAD_LOGIT", "MOE_DEVERR_OUT_OF_BOUNDS", "use_checked_library", "moe_gather_pairs", "moe_mxfp4_expert_rows",
     "moe_combine_pairs", "moe_dispatch_rows", "moe_dispatch_rows_backward", "moe_combine_rows",
     "moe_combine_rows_backward", "moe_route_backward", "mxfp4_matvec", "nvfp4_matvec", "MOE_FLAG_SWIGLU",
+    "MOE_FLAG_ZERO_SKIPPED",
     "MOE_MATVEC_MAX_ROWS",
 ]
 
@@ -33,6 +34,7 @@ MOE_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
 MOE_FLAG_WEIGHT_ON_INPUT = 0x1
 MOE_FLAG_SWIGLU = 0x2
+MOE_FLAG_ZERO_SKIPPED = 0x8
 MOE_MATVEC_MAX_ROWS = 1024
 MOE_DEVERR_BAD_EXPERT_ID = 0x1
 MOE_DEVERR_BAD_SCALE = 0x2
@@ -640,7 +642,7 @@ def moe_route_backward(dweights, ids, weights, E: int, dlogits=None, stream=None
 
 
 def _matvec(name, block, x, blocks, scales, scale2, bias, row_ids, rows_per_x, swiglu, alpha, limit, out_dtype, out,
-            stream):
+            stream, zero_skipped):
     c = _Call(x, stream)
     Tx, K = x.shape
     rows_per_x = int(rows_per_x)
@@ -651,6 +653,9 @@ def _matvec(name, block, x, blocks, scales, scale2, bias, row_ids, rows_per_x, s
     if rows_per_x < 1 or -(-R // rows_per_x) != Tx:
         raise ValueError(f"{name}: {R} rows at {rows_per_x} per row of x do not make the {Tx} rows of x")
     n_out = N // 2 if swiglu else N
+    flags = MOE_FLAG_SWIGLU if swiglu else 0
+    if out is None if zero_skipped is None else zero_skipped:
+        flags |= MOE_FLAG_ZERO_SKIPPED
     if out is None:
         out = c.empty(x, (R, n_out), out_dtype or x.dtype)
     elif not out.is_contiguous():
@@ -662,7 +667,7 @@ def _matvec(name, block, x, blocks, scales, scale2, bias, row_ids, rows_per_x, s
             c.flat(blocks, u8, "blocks", E * N * Kh), c.flat(scales, u8, "scales", E * N * (K // block))]
     if block == 16:
         args.append(c.flat(scale2, f32, "scale2", 2 * E if swiglu else E))
-    args += (c.flat(bias, f32, "bias", E * N), MOE_FLAG_SWIGLU if swiglu else 0, alpha, limit, op, od, c.stream)
+    args += (c.flat(bias, f32, "bias", E * N), flags, alpha, limit, op, od, c.stream)
     lib = _lib or load_library()
     rc = (lib.mxfp4_matvec if block == 32 else lib.nvfp4_matvec)(*args)
     if rc:
@@ -671,22 +676,26 @@ def _matvec(name, block, x, blocks, scales, scale2, bias, row_ids, rows_per_x, s
 
 
 def mxfp4_matvec(x, blocks, scales, bias=None, row_ids=None, rows_per_x: int = 1, swiglu: bool = False,
-                 alpha: float = 1.702, limit: float = 7.0, out_dtype=None, out=None, stream=None):
+                 alpha: float = 1.702, limit: float = 7.0, out_dtype=None, out=None, stream=None,
+                 zero_skipped: Optional[bool] = None):
     """Products of a few rows with MXFP4 weights: out[r] = W[row_ids[r]] x[r // rows_per_x] +
     bias[row_ids[r]], followed with `swiglu` by the clamped SwiGLU of the interleaved gate
     and up outputs.  x [*, K] bf16 or fp16; blocks uint8 [E, N, K/2] (or [N, K/2] for one
     matrix), scales [E, N, K/32]; bias fp32 [E, N] or None; row_ids int32 [R] or None (one
-    matrix).  out [R, N] or [R, N/2] of x's type or fp32."""
+    matrix).  out [R, N] or [R, N/2] of x's type or fp32.  Rows whose id is outside [0, E)
+    (moe_route's empty slots among them) become zeros with zero_skipped, by default in an out
+    that this call allocates; in a given out they are left as they were unless it is True."""
     return _matvec("mxfp4_matvec", 32, x, blocks, scales, None, bias, row_ids, rows_per_x, swiglu, alpha, limit,
-                   out_dtype, out, stream)
+                   out_dtype, out, stream, zero_skipped)
 
 
 def nvfp4_matvec(x, blocks, scales, scale2=None, bias=None, row_ids=None, rows_per_x: int = 1, swiglu: bool = False,
-                 alpha: float = 1.702, limit: float = 7.0, out_dtype=None, out=None, stream=None):
+                 alpha: float = 1.702, limit: float = 7.0, out_dtype=None, out=None, stream=None,
+                 zero_skipped: Optional[bool] = None):
     """mxfp4_matvec over NVFP4 weights: E4M3 scales [E, N, K/16] and fp32 scale2 [E] ([E, 2],
     gate and up, with `swiglu`) or None; scale2 multiplies the product before the bias."""
     return _matvec("nvfp4_matvec", 16, x, blocks, scales, scale2, bias, row_ids, rows_per_x, swiglu, alpha, limit,
-                   out_dtype, out, stream)
+                   out_dtype, out, stream, zero_skipped)
 
 
 def moe_token_tile_rows(T: int, H: int, I: int, E: int, k: int, nvfp4: bool = False) -> int:

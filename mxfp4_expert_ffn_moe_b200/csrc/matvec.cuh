@@ -97,6 +97,7 @@ struct Params {
     const float *bias;          // [E, N] or null
     float alpha, limit;
     void *out;                  // [R, N] or [R, N/2]
+    bool zero_skipped;          // rows whose id is outside [0, E) become zeros
     Layout L;
 };
 
@@ -566,6 +567,11 @@ __global__ void __launch_bounds__(T::kThreads, 1) matvec_kernel(const __grid_con
 
     constexpr int kRed = T::kGroupRows * kTok;         // outputs of a group
     const int n_out = kSwiGlu ? q.N / 2 : q.N;
+    if (q.zero_skipped && q.row_ids)
+        for (int r = blockIdx.x; r < q.R; r += gridDim.x)
+            if (sh.ids[r] < 0)
+                for (int i = tid; i < n_out; i += 32 * T::kWarps)
+                    static_cast<Out *>(q.out)[(int64_t)r * n_out + i] = f32_to_elem<Out>(0.0f);
     const int group = warp / T::kSplit, part = warp % T::kSplit, g = lane >> 2, t = lane & 3;
     const int per_row = q.K / (kNv ? 16 : 32);
     const uint32_t ring = ptx::smem_u32(sm) + part / 8 * T::kBoxBytes + (group * T::kGroupRows + lane) * 128;

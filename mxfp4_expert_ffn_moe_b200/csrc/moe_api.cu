@@ -895,7 +895,7 @@ int matvec(const void *x, int x_dtype, int64_t x_stride, int rows_per_x, int64_t
            const int32_t *row_ids, const uint8_t *blocks, const uint8_t *scales, const float *scale2,
            const float *bias, uint32_t flags, float alpha, float limit, void *out, int out_dtype, cudaStream_t s) {
     if (!x || !blocks || !scales || !out) return MOE_ERR_INVALID_ARG;
-    if (flags & ~MOE_FLAG_SWIGLU) return MOE_ERR_INVALID_ARG;
+    if (flags & ~(MOE_FLAG_SWIGLU | MOE_FLAG_ZERO_SKIPPED)) return MOE_ERR_INVALID_ARG;
     const bool swiglu = (flags & MOE_FLAG_SWIGLU) != 0;
     if (R < 1 || rows_per_x < 1 || N < 1 || K < 32 || K % 32 != 0 || E < 1 || (!row_ids && E != 1) || x_stride < 0 ||
         (swiglu && N % 2 != 0))
@@ -907,7 +907,7 @@ int matvec(const void *x, int x_dtype, int64_t x_stride, int rows_per_x, int64_t
         !aligned(scale2, 4) || !aligned(bias, 4) || !aligned(out, dtype_size(out_dtype)))
         return MOE_ERR_INVALID_ARG;
     const moe::mv::Params q{x,      x_stride, rows_per_x, (int)R, (int)N, (int)K, (int)E, row_ids,
-                            scales, scale2,   bias,       alpha,  limit,  out,    {}};
+                            scales, scale2,   bias,       alpha,  limit,  out,    (flags & MOE_FLAG_ZERO_SKIPPED) != 0, {}};
 #define MOE_MATVEC(X, OUT) \
     return swiglu ? launch_matvec<X, OUT, kNv, true>(q, blocks, s) : launch_matvec<X, OUT, kNv, false>(q, blocks, s)
     if (x_dtype == MOE_DTYPE_BF16) {
