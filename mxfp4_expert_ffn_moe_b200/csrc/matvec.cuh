@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) matvec_kernel(const __grid_con
         rs.ref = -1;
         rs.bytes = ptx::smem_u32(sm + q.L.scales) + sbuf * q.L.scale_bytes +
                    ((uint32_t)(e * q.N + tile * T::kRows) * (uint32_t)per_row & 15u) + my_row * q.L.scale_stride;
-        ok = ok && wait_or_fail(sh.failed, sh.scales_full[sbuf], sphase);
+        ok &= wait_or_fail(sh.failed, sh.scales_full[sbuf], sphase);
         float acc[T::kTiles][4];
 #pragma unroll
         for (int m = 0; m < T::kTiles; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.0f;
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) matvec_kernel(const __grid_con
             const int first = c * (T::kStageK / 32) + part;
             const int n = (q.K / 32 - first + T::kSplit - 1) / T::kSplit;        // at least kBlocks in a whole stage
             if (n > 0) make_factors<T, kNv>(factors, rs, first, n, acc);
-            ok = ok && wait_or_fail(sh.failed, sh.full[stage], phase);
+            ok &= wait_or_fail(sh.failed, sh.full[stage], phase);
             const uint32_t w = ring + stage * T::kStageBytes, x = x0 + c * (T::kStageK * 2);
             if (n >= T::kBlocks)
                 multiply_blocks<T, kNv, true>(w, unit, x, factors, n, acc);

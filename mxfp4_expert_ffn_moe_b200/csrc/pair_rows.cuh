@@ -90,6 +90,7 @@ struct PairRows {
 constexpr int kBulkWarps = 4;                          // computing warps; one more issues the copies
 constexpr int kBulkThreads = 32 * (kBulkWarps + 1);
 constexpr int kBulkStages = 4;
+constexpr uint32_t kGaveUp = 1u << 31;                 // beside a stage's bytes: a reader gave up
 
 // The operands, strides in elements; a stage holds `seg` elements of the token's row (a, if
 // it is read) and of each of its k expert rows (rows_in, if they are read).
@@ -184,6 +185,7 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
                 const int h0 = s * b.seg, n = min(b.seg, H - h0);
                 ok = __all_sync(0xFFFFFFFFu, wait_or_fail(failed, empty[stage], phase ^ 1u));
                 if (!ok) break;
+                const int gave_up = *static_cast<volatile int *>(&failed);      // tested below, behind its latency
                 if (lane < 8) {
                     row_s[stage][lane] = r;
                     weight_s[stage][lane] = w;
@@ -211,7 +213,10 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
                         dst += src - (reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15));
                     }
                 }
-                const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, bytes), bar = ptx::smem_u32(&full[stage]);
+                const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, lane == 0 && gave_up ? bytes | kGaveUp : bytes);
+                const uint32_t bar = ptx::smem_u32(&full[stage]);
+                ok = total < kGaveUp;
+                if (!ok) break;
                 __syncwarp();           // the plain stores above come before the arrival
                 if (lane == 0) ptx::mbar_arrive_expect_tx(bar, total);
                 __syncwarp();
@@ -229,14 +234,13 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
     }
 
     int turn = 0;
-    bool ok = true;                     // no wait of this thread gave up
     for (int64_t t = blockIdx.x; t < q.T; t += gridDim.x, turn ^= 1) {
         float dot[KM];
 #pragma unroll
         for (int j = 0; j < KM; ++j) dot[j] = 0.0f;
         for (int s = 0; s < segs; ++s) {
             const int h0 = s * b.seg, n = min(b.seg, H - h0);
-            ok = ok && wait_or_fail(failed, full[stage], phase);
+            wait_or_fail(failed, full[stage], phase);
             const uint8_t *sa = ring + stage * b.stage_bytes;
             int row[KM];
             float w[KM];
@@ -280,7 +284,7 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
                 }
             }
             __syncwarp();
-            if (lane == 0 && ok) ptx::mbar_arrive(ptx::smem_u32(&empty[stage]));
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&empty[stage]));
             if (++stage == b.stages) {
                 stage = 0;
                 phase ^= 1u;

@@ -47,10 +47,12 @@ __device__ __forceinline__ bool ring_wait(uint64_t &bar, uint32_t parity) {
 
 // Wait of a block that shares the flag `failed`: false once a wait gave up (and raised the
 // device error), at once after that unless the phase is over.  A reader whose wait failed
-// runs out over what the buffers hold, without waiting again and without arriving on an
-// `empty` barrier: a stage is then filled again only behind readers that saw it full, so
-// no fill meets one that is under way.  (A test of the flag between the filler's wait and
-// its copy does the same, but lies on the way of every stage: 3% of a long-K matvec.)
+// runs out over what the buffers hold.  Its arrival on `empty` would let a stage be filled
+// over a copy that is still under way, so either it arrives no more (the matvec), or the
+// filler tests `failed`, which is set before such an arrival, between its wait and its copy
+// (the row kernels, whose registers are scarcer: a predicate kept across the reader's loop
+// took up to a third longer on narrow rows.  The test hides behind the making of addresses
+// there; on the matvec's shorter way it cost 3% of long rows).
 __device__ __forceinline__ bool wait_or_fail(int &failed, uint64_t &bar, uint32_t parity) {
     volatile int *flag = &failed;
     if (ptx::mbar_test_wait(ptx::smem_u32(&bar), parity)) return true;
