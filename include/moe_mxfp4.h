@@ -355,6 +355,9 @@ int moe_combine_pairs(const float *y_rows, const int32_t *pair_rows, int64_t T, 
 /* Element types of the calls below. */
 typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 } moe_dtype;
 
+/* A flag of the calls below: rows that the call would leave as they were become zeros. */
+#define MOE_FLAG_ZERO_SKIPPED 0x8u
+
 /*
  * moe_dispatch_rows -- token rows to expert rows.  For pair p = t*k + j with row
  * r = pair_rows[p] and weight s = weights[p] (1 when weights is NULL):
@@ -376,9 +379,10 @@ typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 } moe_dt
  * A pair with pair_rows[p] < 0 is dropped: neither its row nor its weight is read, it adds
  * nothing, its dweights is 0; a token whose pairs are all dropped gets zeros.  An entry
  * >= R is treated so too and raises MOE_DEVERR_OUT_OF_BOUNDS.  Rows that no pair names
- * are left as they were.  The calls that write rows (moe_dispatch_rows,
- * moe_combine_rows_backward) need the entries that are not dropped to be distinct, as
- * moe_permute's are; the others may name a row twice.  Products and sums are fp32 in a
+ * are left as they were, or with MOE_FLAG_ZERO_SKIPPED (the _ex calls) become zeros.  The
+ * calls that write rows (moe_dispatch_rows, moe_combine_rows_backward) need the entries
+ * that are not dropped to be distinct, as moe_permute's are; the others may name a row
+ * twice.  Products and sums are fp32 in a
  * fixed order, every result is rounded once; outputs must not alias inputs.
  * Types: rows_dtype equal to the token side's type, or MOE_DTYPE_F32 (else
  * MOE_ERR_UNSUPPORTED).  Sizes: T, H, R >= 1; 1 <= k <= 8; T*k, R < 2^31; H <= 2^30; pointers
@@ -388,6 +392,9 @@ typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 } moe_dt
 int moe_dispatch_rows(const void *x, int x_dtype, int64_t x_stride, int64_t T, int64_t H, int k,
                       const int32_t *pair_rows, const float *weights, int64_t R, void *rows,
                       int rows_dtype, int64_t rows_stride, void *stream);
+int moe_dispatch_rows_ex(const void *x, int x_dtype, int64_t x_stride, int64_t T, int64_t H, int k,
+                         const int32_t *pair_rows, const float *weights, int64_t R, void *rows,
+                         int rows_dtype, int64_t rows_stride, uint32_t flags, void *stream);
 int moe_dispatch_rows_backward(const void *drows, int rows_dtype, int64_t rows_stride, int64_t T,
                                int64_t H, int k, int64_t R, const int32_t *pair_rows,
                                const float *weights, const void *x, int64_t x_stride, void *dx,
@@ -399,6 +406,11 @@ int moe_combine_rows_backward(const void *dout, int out_dtype, int64_t dout_stri
                               int k, const int32_t *pair_rows, const float *weights, const void *rows,
                               int64_t rows_stride, int64_t R, void *drows, int rows_dtype,
                               int64_t drows_stride, float *dweights, void *stream);
+int moe_combine_rows_backward_ex(const void *dout, int out_dtype, int64_t dout_stride, int64_t T,
+                                 int64_t H, int k, const int32_t *pair_rows, const float *weights,
+                                 const void *rows, int64_t rows_stride, int64_t R, void *drows,
+                                 int rows_dtype, int64_t drows_stride, float *dweights,
+                                 uint32_t flags, void *stream);
 
 /*
  * moe_route_backward -- gradient of moe_route's weights with respect to the router logits:
@@ -441,7 +453,6 @@ int moe_route_backward(const float *dweights, const int32_t *ids, const float *w
  * MOE_ERR_UNSUPPORTED for types.
  */
 #define MOE_FLAG_SWIGLU 0x2u
-#define MOE_FLAG_ZERO_SKIPPED 0x8u    /* rows that the call would leave as they were become zeros */
 #define MOE_MATVEC_MAX_ROWS 1024
 #define MOE_MATVEC_MAX_K 32768
 int mxfp4_matvec(const void *x, int x_dtype, int64_t x_stride, int rows_per_x, int64_t R, int64_t N,

@@ -50,7 +50,7 @@ EXPORTED_SYMBOLS = (
     "mxfp4_dequantize_from_host", "nvfp4_dequantize_from_host", "moe_permute", "moe_token_tile_rows",
     "moe_gather_pairs", "moe_mxfp4_expert_rows", "moe_combine_pairs",
     "moe_dispatch_rows", "moe_dispatch_rows_backward", "moe_combine_rows", "moe_combine_rows_backward",
-    "moe_route_backward", "mxfp4_matvec", "nvfp4_matvec",
+    "moe_dispatch_rows_ex", "moe_combine_rows_backward_ex", "moe_route_backward", "mxfp4_matvec", "nvfp4_matvec",
 )
 PROFILE_STAGES = ("route", "permute", "gather", "gate_up", "down", "combine", "dequant")
 
@@ -142,12 +142,16 @@ def load_library():
     lib.moe_combine_pairs.restype = i32
     lib.moe_dispatch_rows.argtypes = [p, i32, i64, i64, i64, i32, p, p, i64, p, i32, i64, p]
     lib.moe_dispatch_rows.restype = i32
+    lib.moe_dispatch_rows_ex.argtypes = [p, i32, i64, i64, i64, i32, p, p, i64, p, i32, i64, ctypes.c_uint32, p]
+    lib.moe_dispatch_rows_ex.restype = i32
     lib.moe_dispatch_rows_backward.argtypes = [p, i32, i64, i64, i64, i32, i64, p, p, p, i64, p, i32, i64, p, p]
     lib.moe_dispatch_rows_backward.restype = i32
     lib.moe_combine_rows.argtypes = [p, i32, i64, i64, i64, i32, i64, p, p, p, i32, i64, p]
     lib.moe_combine_rows.restype = i32
     lib.moe_combine_rows_backward.argtypes = [p, i32, i64, i64, i64, i32, p, p, p, i64, i64, p, i32, i64, p, p]
     lib.moe_combine_rows_backward.restype = i32
+    lib.moe_combine_rows_backward_ex.argtypes = [p, i32, i64, i64, i64, i32, p, p, p, i64, i64, p, i32, i64, p, ctypes.c_uint32, p]
+    lib.moe_combine_rows_backward_ex.restype = i32
     lib.moe_route_backward.argtypes = [p, p, p, i64, i64, i32, p, p]
     lib.moe_route_backward.restype = i32
     matvec = [p, i32, i64, i32, i64, i64, i64, i64, p, p, p]
@@ -526,23 +530,25 @@ class _Call:
 
 
 def moe_dispatch_rows(x, pair_rows, k: int, weights=None, n_rows: Optional[int] = None, dtype=None, rows=None,
-                      stream=None):
+                      stream=None, zero_skipped: Optional[bool] = None):
     """Token rows to expert rows: rows[pair_rows[t*k + j]] = weights[t, j] * x[t].
     x [T, H] bf16, fp16 or fp32 with any row stride; pair_rows int32 [T*k] (moe_permute's,
     -1 for a dropped pair) or None (row p for pair p); weights fp32 [T, k] or None (1).
     Writes and returns rows [n_rows, H] (T*k rows of x's type unless rows, n_rows or dtype
-    say otherwise); rows that no pair names are left as they were."""
+    say otherwise).  Rows that no pair names become zeros with zero_skipped, by default where
+    this call allocates rows; in given rows they are left as they were unless it is True."""
     c = _Call(x, stream)
     T, H = x.shape
     k = int(k)
+    flags = MOE_FLAG_ZERO_SKIPPED if (rows is None if zero_skipped is None else zero_skipped) else 0
     if rows is None:
         rows = c.empty(x, (T * k if n_rows is None else n_rows, H), dtype or x.dtype)
     R = rows.shape[0]
     xp, xd, xs = c.rows(x, "x", T, H)
     rp, rd, rs = c.rows(rows, "rows", R, H, dtype)
-    rc = (_lib or load_library()).moe_dispatch_rows(
+    rc = (_lib or load_library()).moe_dispatch_rows_ex(
         xp, xd, xs, T, H, k, c.flat(pair_rows, _t.int32, "pair_rows", T * k),
-        c.flat(weights, _t.float32, "weights", T * k), R, rp, rd, rs, c.stream)
+        c.flat(weights, _t.float32, "weights", T * k), R, rp, rd, rs, flags, c.stream)
     if rc:
         raise MoEError("moe_dispatch_rows", rc)
     return rows
@@ -595,15 +601,17 @@ def moe_combine_rows(rows, pair_rows, T: int, k: int, weights=None, dtype=None, 
 
 
 def moe_combine_rows_backward(dout, pair_rows, k: int, weights=None, y_rows=None, n_rows: Optional[int] = None,
-                              dtype=None, drows=None, dweights=None, stream=None):
+                              dtype=None, drows=None, dweights=None, stream=None, zero_skipped: Optional[bool] = None):
     """Gradient of moe_combine_rows: drows[pair_rows[t*k + j]] = weights[t, j] * dout[t] and,
     when the forward pass's y_rows [R, H] is given, dweights[t, j] = <dout[t],
     y_rows[pair_rows[t*k + j]]> (fp32 [T, k]).  drows is [R, H] of y_rows' type (n_rows, or
-    T*k, rows of dout's type without y_rows); rows that no pair names are left as they
-    were.  Returns drows, or (drows, dweights)."""
+    T*k, rows of dout's type without y_rows).  Rows that no pair names become zeros with
+    zero_skipped, by default where this call allocates drows; in a given drows they are left
+    as they were unless it is True.  Returns drows, or (drows, dweights)."""
     c = _Call(dout, stream)
     T, H = dout.shape
     k = int(k)
+    flags = MOE_FLAG_ZERO_SKIPPED if (drows is None if zero_skipped is None else zero_skipped) else 0
     if drows is None:
         n = y_rows.shape[0] if y_rows is not None else T * k if n_rows is None else n_rows
         drows = c.empty(dout, (n, H), dtype or (dout.dtype if y_rows is None else y_rows.dtype))
@@ -615,10 +623,10 @@ def moe_combine_rows_backward(dout, pair_rows, k: int, weights=None, y_rows=None
     op, od, os_ = c.rows(dout, "dout", T, H)
     dp, dd, ds = c.rows(drows, "drows", R, H, dtype)
     yp, _, ys = c.rows(y_rows, "y_rows", R, H, drows.dtype)
-    rc = (_lib or load_library()).moe_combine_rows_backward(
+    rc = (_lib or load_library()).moe_combine_rows_backward_ex(
         op, od, os_, T, H, k, c.flat(pair_rows, _t.int32, "pair_rows", T * k),
         c.flat(weights, _t.float32, "weights", T * k), yp, ys, R, dp, dd, ds,
-        c.flat(dweights, _t.float32, "dweights", T * k), c.stream)
+        c.flat(dweights, _t.float32, "dweights", T * k), flags, c.stream)
     if rc:
         raise MoEError("moe_combine_rows_backward", rc)
     return drows if y_rows is None else (drows, dweights)

@@ -33,6 +33,7 @@
 #include "split.cuh"
 #include "route.cuh"
 #include "router.cuh"
+#include "unnamed_rows.cuh"
 
 namespace {
 
@@ -687,6 +688,28 @@ bool pair_sizes_ok(int64_t T, int64_t H, int k, int64_t R) {
            H <= (int64_t(1) << 30);
 }
 
+// Blocks of a kernel that the registers of an SM hold, 8 at most.  A grid of more than are
+// resident leaves some for a second round: rows of 200 fp32 6.9 us for 9.4, of 333 bf16 16.8 for 19.1.
+int blocks_by_registers(const void *kernel, int threads) {
+    cudaFuncAttributes a{};
+    if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess) cudaGetLastError();
+    const int regs = (a.numRegs + 7) / 8 * 8 * threads;
+    return regs > 0 ? std::max(1, std::min(8, 65536 / regs)) : 8;
+}
+
+// Blocks of a call with room for `places` at once, and its shared memory.  Where rows are to
+// be zeroed (b.zero_blocks), a block per 256 KB of the buffer does so, but no more than can be
+// spared without another round of tokens (12 of 444 at 8192 tokens), and one at least.  With
+// four at most, 4096 x 8 rows of 64 took 16.4 us for 13.
+int64_t spread_grid(const moe::PairRows &q, moe::PairBulk &b, int64_t row_bytes, int64_t places, int &smem) {
+    smem = b.stages * b.stage_bytes;
+    if (!b.zero_blocks) return std::min(q.T, places);
+    b.zero_room = smem = std::max(smem, 4096);
+    const int64_t spare = places - moe::ceil_div(q.T, moe::ceil_div(q.T, places));
+    b.zero_blocks = (int)std::max<int64_t>(1, std::min<int64_t>({q.R * row_bytes / (256 * 1024), spare, 32}));
+    return b.zero_blocks + std::min(q.T, std::max<int64_t>(1, places - b.zero_blocks));
+}
+
 // Shared memory: stages of at most 32 KB (the row split into equal segments, multiples of 8
 // elements), 2 to 4 of them within 72 KB, so that three blocks share an SM and some 170 KB
 // are on their way to each.  Off 16-byte words a row takes up to 30 bytes more.
@@ -700,11 +723,12 @@ int launch_pairs(const moe::PairRows &q, moe::PairBulk b, cudaStream_t s) {
     b.row_slot = slot(row);
     b.stage_bytes = (b.a_slot + q.k * b.row_slot + 127) / 128 * 128;
     b.stages = std::max(2, std::min(72 * 1024 / b.stage_bytes, moe::kBulkStages));
-    const int smem = b.stages * b.stage_bytes;
     auto kernel = moe::pair_bulk_kernel<Tok, Row, KM, kSum, kDot, kWords>;
+    static const int by_registers = blocks_by_registers(reinterpret_cast<const void *>(kernel), moe::kBulkThreads);
+    const int64_t per_sm = std::min<int64_t>(by_registers, 227 * 1024 / (b.stages * b.stage_bytes + 2048));
+    int smem;
+    const int64_t grid = spread_grid(q, b, q.H * sizeof(Row), sm_count() * per_sm, smem);
     if (!ensure_smem_attr(reinterpret_cast<const void *>(kernel), smem)) return MOE_ERR_CUDA;
-    const int64_t per_sm = std::min<int64_t>(8, 227 * 1024 / (smem + 2048));
-    const int64_t grid = std::min<int64_t>(q.T, sm_count() * per_sm);
     StageScope scope(kSum ? MOE_STAGE_COMBINE : MOE_STAGE_GATHER, s);
     launch_pdl(kernel, dim3((unsigned)grid), dim3(moe::kBulkThreads), smem, s, q, b);
     return launch_check();
@@ -718,11 +742,29 @@ int launch_copy(const moe::PairRows &q, moe::PairBulk b, int elem, cudaStream_t 
     b.seg = (int)(moe::ceil_div(moe::ceil_div(q.H, segs), 8) * 8);
     b.stage_bytes = (b.seg * elem + 127) / 128 * 128;
     b.stages = moe::kCopyStages;
-    const int smem = b.stages * b.stage_bytes;
+    int smem;
+    const int64_t grid = spread_grid(q, b, q.H * elem, sm_count() * 3, smem);
     if (!ensure_smem_attr(reinterpret_cast<const void *>(moe::copy_rows_kernel), smem)) return MOE_ERR_CUDA;
-    const int64_t grid = std::min<int64_t>(q.T, sm_count() * 3);
     StageScope scope(MOE_STAGE_GATHER, s);
-    launch_pdl(moe::copy_rows_kernel, dim3((unsigned)grid), dim3(32), smem, s, q, b, elem);
+    launch_pdl(moe::copy_rows_kernel, dim3((unsigned)grid), dim3(b.zero_blocks ? moe::kCopyThreads : 32), smem, s, q,
+               b, elem);
+    return launch_check();
+}
+
+// Up to so many pairs the rows that none names are zeroed by blocks of the spread, which costs no
+// launch (2.2 us of the host's time; calls of fewer pairs are bound by that).  Beyond, their
+// reading of all pairs beside the spread's traffic is too slow, and a launch behind it is not
+// seen: 32768 x 4 rows of 2880 bf16 178 us without zeros, 225 by such blocks, 187 by the launch.
+constexpr int64_t kZeroBesidePairs = 32768;
+
+// Zeros behind a spread: a cluster per 8 SMs.
+template <class Unit>
+int launch_zero(const moe::PairRows &q, void *rows, int64_t stride, size_t elem, cudaStream_t s) {
+    const int64_t per = sizeof(Unit) / elem;
+    const int clusters = std::max(1, sm_count() / moe::kZeroCluster);
+    StageScope scope(MOE_STAGE_GATHER, s);
+    launch_pdl_cluster(moe::zero_unnamed_kernel<Unit>, dim3((unsigned)(clusters * moe::kZeroCluster)), dim3(moe::kZeroThreads), 0,
+                       moe::kZeroCluster, s, q, static_cast<Unit *>(rows), stride / per, q.H / per);
     return launch_check();
 }
 
@@ -755,10 +797,12 @@ int run_pairs(const moe::PairRows &q, const moe::PairBulk &b, int tok, int row, 
     });
 }
 
-// rows[r(p)] = s_p a[t]; with src: dots[p] = <a[t], src[r(p)]>.
+// rows[r(p)] = s_p a[t]; with src: dots[p] = <a[t], src[r(p)]>; with MOE_FLAG_ZERO_SKIPPED the
+// rows that no pair names become zeros.
 int spread(const void *a, int a_dtype, int64_t a_stride, int64_t T, int64_t H, int k, const int32_t *pair_rows,
            const float *weights, const void *src, int64_t src_stride, int64_t R, void *rows, int rows_dtype,
-           int64_t rows_stride, float *dots, cudaStream_t s) {
+           int64_t rows_stride, float *dots, uint32_t flags, cudaStream_t s) {
+    if (flags & ~MOE_FLAG_ZERO_SKIPPED) return MOE_ERR_INVALID_ARG;
     if (!a || !rows || (src == nullptr) != (dots == nullptr)) return MOE_ERR_INVALID_ARG;
     if (!pair_sizes_ok(T, H, k, R) || !dtype_size(a_dtype) || !dtype_size(rows_dtype)) return MOE_ERR_INVALID_ARG;
     if (!pair_rows && R < T * k) return MOE_ERR_INVALID_ARG;
@@ -767,12 +811,20 @@ int spread(const void *a, int a_dtype, int64_t a_stride, int64_t T, int64_t H, i
         !aligned(rows, dtype_size(rows_dtype)) || !aligned(pair_rows, 4) || !aligned(weights, 4) || !aligned(dots, 4))
         return MOE_ERR_INVALID_ARG;
     const moe::PairRows q{T, H, R, k, pair_rows, weights, dots};
-    const moe::PairBulk b{a, src, rows, a_stride, src_stride, rows_stride, 0, 0, 0, 0, 0};
+    moe::PairBulk b{a, src, rows, a_stride, src_stride, rows_stride, 0, 0, 0, 0, 0, 0, 0};
     const bool words = rows_of_words(H, {{a, a_stride, dtype_size(a_dtype)},
                                          {src, src_stride, dtype_size(rows_dtype)},
                                          {rows, rows_stride, dtype_size(rows_dtype)}});
-    if (words && !weights && !dots && a_dtype == rows_dtype) return launch_copy(q, b, (int)dtype_size(a_dtype), s);
-    return run_pairs<false>(q, b, a_dtype, rows_dtype, words, s);
+    // rows can only be left out where pairs can be dropped, or R passes the pairs
+    const bool zero = (flags & MOE_FLAG_ZERO_SKIPPED) && (pair_rows || R > T * k), behind = zero && T * k > kZeroBesidePairs;
+    if (zero && !behind) b.zero_blocks = 1;
+    const int rc = words && !weights && !dots && a_dtype == rows_dtype ? launch_copy(q, b, (int)dtype_size(a_dtype), s)
+                                                                       : run_pairs<false>(q, b, a_dtype, rows_dtype, words, s);
+    if (rc != MOE_OK || !behind) return rc;
+    const size_t size = dtype_size(rows_dtype);
+    return words ? launch_zero<uint4>(q, rows, rows_stride, size, s)
+           : size == 4 ? launch_zero<uint32_t>(q, rows, rows_stride, size, s)
+                       : launch_zero<uint16_t>(q, rows, rows_stride, size, s);
 }
 
 // out[t] = sum_j s_p rows[r(p)]; with a: dots[p] = <a[t], rows[r(p)]>.
@@ -787,7 +839,7 @@ int sum_rows(const void *rows, int rows_dtype, int64_t rows_stride, int64_t T, i
         !aligned(out, dtype_size(out_dtype)) || !aligned(pair_rows, 4) || !aligned(weights, 4) || !aligned(dots, 4))
         return MOE_ERR_INVALID_ARG;
     const moe::PairRows q{T, H, R, k, pair_rows, weights, dots};
-    const moe::PairBulk b{a, rows, out, a_stride, rows_stride, out_stride, 0, 0, 0, 0, 0};
+    const moe::PairBulk b{a, rows, out, a_stride, rows_stride, out_stride, 0, 0, 0, 0, 0, 0, 0};
     const bool words = rows_of_words(H, {{rows, rows_stride, dtype_size(rows_dtype)},
                                          {a, a_stride, dtype_size(out_dtype)},
                                          {out, out_stride, dtype_size(out_dtype)}});
@@ -1092,12 +1144,19 @@ int moe_combine_pairs(const float *y_rows, const int32_t *pair_rows, int64_t T, 
     return launch_check();
 }
 
+int moe_dispatch_rows_ex(const void *x, int x_dtype, int64_t x_stride, int64_t T, int64_t H, int k,
+                         const int32_t *pair_rows, const float *weights, int64_t R, void *rows, int rows_dtype,
+                         int64_t rows_stride, uint32_t flags, void *stream) {
+    NvtxRange nvtx("moe_dispatch_rows");
+    return spread(x, x_dtype, x_stride, T, H, k, pair_rows, weights, nullptr, 0, R, rows, rows_dtype, rows_stride,
+                  nullptr, flags, (cudaStream_t)stream);
+}
+
 int moe_dispatch_rows(const void *x, int x_dtype, int64_t x_stride, int64_t T, int64_t H, int k,
                       const int32_t *pair_rows, const float *weights, int64_t R, void *rows, int rows_dtype,
                       int64_t rows_stride, void *stream) {
-    NvtxRange nvtx("moe_dispatch_rows");
-    return spread(x, x_dtype, x_stride, T, H, k, pair_rows, weights, nullptr, 0, R, rows, rows_dtype, rows_stride,
-                  nullptr, (cudaStream_t)stream);
+    return moe_dispatch_rows_ex(x, x_dtype, x_stride, T, H, k, pair_rows, weights, R, rows, rows_dtype, rows_stride, 0u,
+                                stream);
 }
 
 int moe_dispatch_rows_backward(const void *drows, int rows_dtype, int64_t rows_stride, int64_t T, int64_t H, int k,
@@ -1117,13 +1176,21 @@ int moe_combine_rows(const void *rows, int rows_dtype, int64_t rows_stride, int6
                     out_stride, nullptr, (cudaStream_t)stream);
 }
 
+int moe_combine_rows_backward_ex(const void *dout, int out_dtype, int64_t dout_stride, int64_t T, int64_t H, int k,
+                                 const int32_t *pair_rows, const float *weights, const void *rows,
+                                 int64_t rows_stride, int64_t R, void *drows, int rows_dtype, int64_t drows_stride,
+                                 float *dweights, uint32_t flags, void *stream) {
+    NvtxRange nvtx("moe_combine_rows_backward");
+    return spread(dout, out_dtype, dout_stride, T, H, k, pair_rows, weights, rows, rows_stride, R, drows, rows_dtype,
+                  drows_stride, dweights, flags, (cudaStream_t)stream);
+}
+
 int moe_combine_rows_backward(const void *dout, int out_dtype, int64_t dout_stride, int64_t T, int64_t H, int k,
                               const int32_t *pair_rows, const float *weights, const void *rows, int64_t rows_stride,
                               int64_t R, void *drows, int rows_dtype, int64_t drows_stride, float *dweights,
                               void *stream) {
-    NvtxRange nvtx("moe_combine_rows_backward");
-    return spread(dout, out_dtype, dout_stride, T, H, k, pair_rows, weights, rows, rows_stride, R, drows, rows_dtype,
-                  drows_stride, dweights, (cudaStream_t)stream);
+    return moe_combine_rows_backward_ex(dout, out_dtype, dout_stride, T, H, k, pair_rows, weights, rows, rows_stride, R,
+                                        drows, rows_dtype, drows_stride, dweights, 0u, stream);
 }
 
 int moe_route_backward(const float *dweights, const int32_t *ids, const float *weights, int64_t T, int64_t E, int k,

@@ -30,6 +30,8 @@
 #pragma once
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "ring.cuh"
 #include "sm100_ptx.cuh"
@@ -100,6 +102,7 @@ struct PairBulk {
     int64_t a_stride, rows_stride, out_stride;
     int seg, stages;
     int a_slot, row_slot, stage_bytes;      // room for the token's row, an expert row, all of them
+    int zero_blocks, zero_room;             // spread: blocks that zero rows, and the rows they can mark at once
 };
 
 // Lane j < k of a warp: the expert row of pair j of token t (-1: dropped) and its weight.
@@ -114,6 +117,61 @@ __device__ __forceinline__ void load_pair(const PairRows &q, int64_t t, int lane
         raise_device_error(MOE_DEVERR_OUT_OF_BOUNDS);
     else
         r = row < 0 ? -1 : (int)row;
+}
+
+// Zeros in the rows of a spread's buffer that no pair names, by blocks of their own (the
+// first of the grid) beside those that write the others.  Such a block has a share of the
+// rows: it reads all of pair_rows, marks its rows that are named in shared memory, a byte
+// each (`marks`, room for `room`), and zeroes the rest.  A row is stored by units: 16-byte
+// words or elements.
+// They read while the others write, so what they cost shows only where a call is shorter than
+// their reading of many pairs (without / with them): dispatch of 4096 x 8 rows of 64 bf16
+// 5.9 / 14 us, 4000 x 4 of 512 fp16 5.6 / 7.4; 8192 x 4 of 2880 44.2 / 44.6, combine's gradient
+// there 75.4 / 76.2.  Marks as bits, set by shared atomics, took up to 85 us; a fill of the whole
+// buffer 30 us there.  Calls of more pairs launch unnamed_rows.cuh's kernel instead.
+template <class Unit>
+__device__ __forceinline__ void zero_unnamed(const PairRows &q, Unit *rows, int64_t stride, int64_t units, int share, int shares,
+                                             uint8_t *marks, int room, int threads) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, P = (int)q.T * q.k, R = (int)q.R;
+    const int lo = (int)((int64_t)R * share / shares), hi = (int)((int64_t)R * (share + 1) / shares);
+    const bool wide = (reinterpret_cast<uintptr_t>(q.pair_rows) & 15u) == 0;
+    for (int base = lo; base < hi; base += min(room, hi - base)) {
+        const int n = min(room, hi - base);
+        const auto mark = [&](int r) {
+            const unsigned at = (unsigned)r - (unsigned)base;      // past n for negative entries too
+            if (at < (unsigned)n) marks[at] = 1;
+        };
+        __syncthreads();
+        for (int i = tid; i < n; i += threads) marks[i] = !q.pair_rows && i < P - base;     // no pair_rows: pair p has row p
+        __syncthreads();
+        if (q.pair_rows) {
+            constexpr int kWords = 8;                      // 16-byte words in flight a thread
+            const int words = wide ? P / 4 : 0;
+            for (int i = tid; i < words; i += kWords * threads) {
+                int4 v[kWords];
+#pragma unroll
+                for (int u = 0; u < kWords; ++u)
+                    v[u] = i + u * threads < words ? __ldg(reinterpret_cast<const int4 *>(q.pair_rows) + i + u * threads)
+                                                   : make_int4(-1, -1, -1, -1);
+#pragma unroll
+                for (int u = 0; u < kWords; ++u) {
+                    mark(v[u].x);
+                    mark(v[u].y);
+                    mark(v[u].z);
+                    mark(v[u].w);
+                }
+            }
+            for (int i = 4 * words + tid; i < P; i += min(threads, P - i)) mark(__ldg(q.pair_rows + i));
+        }
+        __syncthreads();
+        for (int i = 32 * warp; i < n; i += threads) {
+            unsigned left = __ballot_sync(0xFFFFFFFFu, i + lane < n && !marks[i + lane]);
+            for (; left; left &= left - 1) {
+                Unit *row = rows + (int64_t)(base + i + __ffs(left) - 1) * stride;
+                for (int64_t c = lane; c < units; c += 32) row[c] = Unit{};
+            }
+        }
+    }
 }
 
 // The 16-byte granules of [p, p + n * sizeof(T)) inside the tensor [base, end): what a bulk
@@ -143,10 +201,14 @@ __device__ __forceinline__ void granules(const T *p, int n, const T *base, const
     bytes = hi > lo ? (uint32_t)(hi - lo) : 0u;
 }
 
-// kWords: every row and segment of every operand lies on 16-byte words.
+// kWords: every row and segment of every operand lies on 16-byte words.  The spreads' registers
+// are bounded to eight blocks an SM, five with the dots: left to the compiler they spill beside
+// the zeroing blocks' (combine's gradient of 8192 x 4 x 2880 78 us for 76), and five blocks of the
+// plain spread are too few for short rows (131072 x 8 of 64 144 us for 115).  The sums are best
+// left alone.
 template <class Tok, class Row, int KM, bool kSum, bool kDot, bool kWords>
-__global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_constant__ PairRows q,
-                                                                 const __grid_constant__ PairBulk b) {
+__global__ void __launch_bounds__(kBulkThreads, kSum ? 0 : kDot ? 5 : 8)
+    pair_bulk_kernel(const __grid_constant__ PairRows q, const __grid_constant__ PairBulk b) {
     constexpr bool kReadsA = !kSum || kDot, kReadsRows = kSum || kDot;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ uint64_t full[kBulkStages], empty[kBulkStages];
@@ -155,6 +217,16 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
     __shared__ float part[2][kBulkWarps][KM];
     __shared__ int failed;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int zero_blocks = kSum ? 0 : b.zero_blocks, block = (int)blockIdx.x - zero_blocks, blocks = (int)gridDim.x - zero_blocks;
+    if (block < 0) {
+        pdl_wait();
+        pdl_trigger();
+        using Unit = std::conditional_t<kWords, uint4, std::conditional_t<sizeof(Row) == 4, uint32_t, uint16_t>>;
+        constexpr int per = sizeof(Unit) / sizeof(Row);
+        zero_unnamed(q, static_cast<Unit *>(b.out), b.out_stride / per, q.H / per, blockIdx.x, zero_blocks,
+                     ring, b.zero_room, kBulkThreads);
+        return;
+    }
     if (tid < kBulkStages * 8) row_s[tid / 8][tid % 8] = -1;      // at all times a row of the buffer or none
     if (tid == 0) {
         for (int i = 0; i < b.stages; ++i) {
@@ -177,10 +249,10 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
         const Row *const r0 = static_cast<const Row *>(b.rows_in), *const r1 = r0 + (q.R - 1) * b.rows_stride + q.H;
         int r, next_r;
         float w, next_w;
-        load_pair(q, blockIdx.x, lane, r, w);
+        load_pair(q, block, lane, r, w);
         bool ok = true;
-        for (int64_t t = blockIdx.x; t < q.T && ok; t += gridDim.x) {
-            load_pair(q, t + gridDim.x, lane, next_r, next_w);
+        for (int64_t t = block; t < q.T && ok; t += blocks) {
+            load_pair(q, t + blocks, lane, next_r, next_w);
             for (int s = 0; s < segs; ++s) {
                 const int h0 = s * b.seg, n = min(b.seg, H - h0);
                 ok = __all_sync(0xFFFFFFFFu, wait_or_fail(failed, empty[stage], phase ^ 1u));
@@ -234,7 +306,7 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
     }
 
     int turn = 0;
-    for (int64_t t = blockIdx.x; t < q.T; t += gridDim.x, turn ^= 1) {
+    for (int64_t t = block; t < q.T; t += blocks, turn ^= 1) {
         float dot[KM];
 #pragma unroll
         for (int j = 0; j < KM; ++j) dot[j] = 0.0f;
@@ -312,14 +384,25 @@ __global__ void __launch_bounds__(kBulkThreads) pair_bulk_kernel(const __grid_co
 
 // The spread of unweighted rows of one type, on 16-byte words: rows[r(p)] = a[t] bit for bit,
 // so nothing but copies.  One warp a block: a bulk copy brings a segment of a token's row
-// to shared memory, lanes j < k each send it on to their expert row.
+// to shared memory, lanes j < k each send it on to their expert row.  Blocks that zero rows
+// work with all of kCopyThreads (the launch has 32 where there are none).
 constexpr int kCopyStages = 4;
+constexpr int kCopyThreads = 128;
 
-__global__ void __launch_bounds__(32) copy_rows_kernel(const __grid_constant__ PairRows q, const __grid_constant__ PairBulk b,
+__global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const __grid_constant__ PairRows q, const __grid_constant__ PairBulk b,
                                                        int elem) {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ uint64_t full[kCopyStages];
+    const int block = (int)blockIdx.x - b.zero_blocks, blocks = (int)gridDim.x - b.zero_blocks;
+    if (block < 0) {
+        pdl_wait();
+        pdl_trigger();
+        zero_unnamed(q, static_cast<uint4 *>(b.out), b.out_stride * elem / 16, q.H * elem / 16, blockIdx.x, b.zero_blocks,
+                     ring, b.zero_room, kCopyThreads);
+        return;
+    }
     const int lane = threadIdx.x, segs = (int)((q.H + b.seg - 1) / b.seg);
+    if (lane >= 32) return;
     if (lane == 0) {
         for (int i = 0; i < kCopyStages; ++i) ptx::mbar_init(ptx::smem_u32(&full[i]), 1);
         ptx::fence_mbarrier_init();
@@ -328,7 +411,7 @@ __global__ void __launch_bounds__(32) copy_rows_kernel(const __grid_constant__ P
     pdl_wait();
     pdl_trigger();
     // the next segment to fetch, its stage and that stage's parity; lane 0 issues the copy
-    int64_t ft = blockIdx.x;
+    int64_t ft = block;
     int fs = 0, fstage = 0;
     uint32_t fphase = 0;
     const auto bytes_of = [&](int seg) { return (uint32_t)(min(b.seg, (int)q.H - seg * b.seg) * elem); };
@@ -344,7 +427,7 @@ __global__ void __launch_bounds__(32) copy_rows_kernel(const __grid_constant__ P
         if (fstage == 0) fphase ^= 1u;
         if (++fs == segs) {
             fs = 0;
-            ft += gridDim.x;
+            ft += blocks;
         }
     };
     for (int i = 0; i < kCopyStages - 1; ++i) fetch();
@@ -352,9 +435,9 @@ __global__ void __launch_bounds__(32) copy_rows_kernel(const __grid_constant__ P
     uint32_t phase = 0;
     float w;
     bool ok = true;
-    load_pair(q, blockIdx.x, lane, r, w);
-    for (int64_t t = blockIdx.x; t < q.T && ok; t += gridDim.x, r = next_r) {
-        load_pair(q, t + gridDim.x, lane, next_r, w);
+    load_pair(q, block, lane, r, w);
+    for (int64_t t = block; t < q.T && ok; t += blocks, r = next_r) {
+        load_pair(q, t + blocks, lane, next_r, w);
         for (int s = 0; s < segs && ok; ++s) {
             ok = __all_sync(0xFFFFFFFFu, ring_wait(full[stage], phase));
             if (ok && r >= 0)

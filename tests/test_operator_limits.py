@@ -28,3 +28,12 @@ def test_a_number_of_pairs_past_32_or_64_bits_is_refused(lib, T, k):
     assert lib.moe_gather_pairs(P, T, 64, k, P, P, P, P, 16, P, P, P, None) == INVALID
     assert lib.moe_mxfp4_workspace_size(T, 128, 128, 16, k) == 0
     assert lib.moe_token_tile_rows(T, 128, 128, 16, k, 0) == INVALID
+
+
+def test_flags_of_the_calls_that_write_expert_rows(lib):
+    for flags in (1, 2, 4, 16, 9):
+        assert lib.moe_dispatch_rows_ex(P, BF16, 64, 8, 64, 2, P, P, 16, P, BF16, 64, flags, None) == INVALID
+        assert lib.moe_combine_rows_backward_ex(P, BF16, 64, 8, 64, 2, P, P, P, 64, 16, P, BF16, 64, P, flags, None) == INVALID
+    # the other checks come before any CUDA call with a good flag too
+    assert lib.moe_dispatch_rows_ex(None, BF16, 64, 8, 64, 2, P, P, 16, P, BF16, 64, moe.MOE_FLAG_ZERO_SKIPPED, None) == INVALID
+    assert lib.moe_combine_rows_backward_ex(P, BF16, 64, 8, 64, 2, P, P, P, 64, 16, P, BF16, 63, P, moe.MOE_FLAG_ZERO_SKIPPED, None) == INVALID
