@@ -441,12 +441,15 @@ int moe_route_backward(const float *dweights, const int32_t *ids, const float *w
  *   out      of out_dtype: x_dtype or MOE_DTYPE_F32
  * Sums in fp32, one rounding.  A row whose id falls outside [0, E) raises
  * MOE_DEVERR_BAD_EXPERT_ID and is left unwritten, or with MOE_FLAG_ZERO_SKIPPED becomes a
- * row of zeros; an invalid scale byte that is read makes its outputs
- * NaN and raises MOE_DEVERR_BAD_SCALE.  bf16 values below 2^-31 of the largest finite one
- * of their row of x count to within 2^-39 of that, and an E8M0 block scaled 2^127 or more
- * below another of its row may count as 0.  Meant for decode, where each weight
- * byte serves few rows and HBM bounds the product: weights are read once for every 8
- * rows of an expert.  Sizes: 1 <= R <= MOE_MATVEC_MAX_ROWS; 1 <= E <= 256; N <= 2^24;
+ * row of zeros; an invalid scale byte that is read makes its outputs NaN and raises
+ * MOE_DEVERR_BAD_SCALE.  bf16 values below 2^-31 of the largest finite one of their row of
+ * x count to within 2^-39 of that.  Sums are kept relative to the largest E8M0 scale of a
+ * stretch of the row: a block scaled 2^100 or more below it may lose bits and from 2^127 on
+ * may count as 0, which shows only where the large scale stands over zero codes.
+ * Meant for decode, where each weight byte serves few rows and HBM bounds the product:
+ * weights are read once for every tile of rows of an expert, 8 rows while K <= 5280
+ * (nvfp4) or 6752 (mxfp4), fewer beyond (their x takes shared memory): 3 to 8 at K = 8192,
+ * 2 to 5 at 14336, 1 or 2 at 32768.  Sizes: 1 <= R <= MOE_MATVEC_MAX_ROWS; 1 <= E <= 256; N <= 2^24;
  * K <= MOE_MATVEC_MAX_K; E * N < 2^31 (beyond: MOE_ERR_UNSUPPORTED); K % 32 == 0; N even with
  * MOE_FLAG_SWIGLU.  x, blocks and scales 16-byte aligned, x_stride a multiple of 8.
  * Errors: MOE_ERR_INVALID_ARG for null pointers, sizes, alignment, flags;

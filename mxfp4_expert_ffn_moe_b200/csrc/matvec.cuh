@@ -20,7 +20,7 @@
 //  * NVFP4 scales multiply the weights in f16 (exact).  E8M0 scales do not fit f16; they
 //    multiply the fp32 sums of their 32-element block, relative to a scale of the warp's
 //    slice of the row, so that no intermediate overflows before the result does (blocks
-//    2^127 or more below that scale drop out).  Each warp turns the scale bytes of its blocks
+//    2^100 below that scale may lose bits to fp32's subnormals, from 2^127 they drop out).  Each warp turns the scale bytes of its blocks
 //    into factors once per stage, a row to a lane, instead of in each lane that uses them.
 //  * Weights arrive as TMA boxes of 128 bytes x the item's rows, 128-byte swizzled (the 8
 //    rows x 4 words of a fragment load then fall into 32 different banks), into a ring of
