@@ -518,8 +518,10 @@ class _Call:
         if t is None:
             return None, 0, 0
         code = _DTYPE_CODES.get(t.dtype)
+        if code is None:
+            code = _dtype_code(t.dtype, name)                  # refuses
         stride = t.stride()
-        if (code is None or t.shape != (n, width) or t.get_device() != self.device or (dtype is not None and
+        if (t.shape != (n, width) or t.get_device() != self.device or (dtype is not None and
                 t.dtype is not dtype) or (stride[1] != 1 and width > 1)):
             raise ValueError(f"{name}: expected a [{n}, {width}] tensor of {dtype or 'bfloat16, float16 or float32'} with "
                              f"contiguous rows on cuda:{self.device}, got {t.dtype} {tuple(t.shape)} on {t.device} with "

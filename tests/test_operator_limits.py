@@ -37,3 +37,18 @@ def test_flags_of_the_calls_that_write_expert_rows(lib):
     # the other checks come before any CUDA call with a good flag too
     assert lib.moe_dispatch_rows_ex(None, BF16, 64, 8, 64, 2, P, P, 16, P, BF16, 64, moe.MOE_FLAG_ZERO_SKIPPED, None) == INVALID
     assert lib.moe_combine_rows_backward_ex(P, BF16, 64, 8, 64, 2, P, P, P, 64, 16, P, BF16, 63, P, moe.MOE_FLAG_ZERO_SKIPPED, None) == INVALID
+
+
+def test_the_types_that_rows_may_have():
+    # the mapping and the refusal that every call's rows go through
+    torch = pytest.importorskip("torch")
+    moe._dtype_code(torch.float32, "t")                       # imports torch into the binding
+    call = object.__new__(moe._Call)
+    call.device, call.side = -1, None
+    for dtype, code in ((torch.bfloat16, 0), (torch.float16, 1), (torch.float32, 2)):
+        assert call.rows(torch.zeros((3, 4), dtype=dtype), "x", 3, 4)[1:] == (code, 4)
+    for dtype in (torch.float64, torch.int32, torch.uint8):
+        with pytest.raises(ValueError, match="x: expected bfloat16, float16 or float32"):
+            call.rows(torch.zeros((3, 4), dtype=dtype), "x", 3, 4)
+    with pytest.raises(ValueError, match="tensor of torch.float16"):
+        call.rows(torch.zeros((3, 4)), "x", 3, 4, torch.float16)
