@@ -379,7 +379,8 @@ typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 } moe_dt
  * A pair with pair_rows[p] < 0 is dropped: neither its row nor its weight is read, it adds
  * nothing, its dweights is 0; a token whose pairs are all dropped gets zeros.  An entry
  * >= R is treated so too and raises MOE_DEVERR_OUT_OF_BOUNDS.  Rows that no pair names
- * are left as they were, or with MOE_FLAG_ZERO_SKIPPED (the _ex calls) become zeros.  The
+ * are left as they were, or become zeros: the _ex calls are the same with flags, 0 or
+ * MOE_FLAG_ZERO_SKIPPED (anything else MOE_ERR_INVALID_ARG).  The
  * calls that write rows (moe_dispatch_rows, moe_combine_rows_backward) need the entries
  * that are not dropped to be distinct, as moe_permute's are; the others may name a row
  * twice.  Products and sums are fp32 in a

@@ -122,10 +122,11 @@ def test_an_entry_past_the_buffer_leaves_its_row_zero(moe_gpu):
     assert torch.equal(rows, want)
 
 
-def test_pair_rows_at_any_address_on_a_stream_and_in_a_graph(moe_gpu):
+@pytest.mark.parametrize("T,k", [(901, 3), (15000, 3)], ids=["beside", "behind"])        # past 32768 pairs: a launch of their own
+def test_pair_rows_at_any_address_on_a_stream_and_in_a_graph(moe_gpu, T, k):
     import torch
     moe = moe_gpu
-    T, k, H = 901, 3, 48
+    H = 48
     pair_rows, w, R, g = _case(T, k, 8, H, 0.1, seed=9)
     x = _randn((T, H), "float32", g)
     want = moe.moe_dispatch_rows(x, pair_rows, k, weights=w)
