@@ -32,14 +32,16 @@
 // 32 elements of every stage; their sums are joined in warp order, so the same call gives
 // the same bits.
 //
-// Measured (device time, gate_up of 64 tokens over 128 experts of 5760 x 2880, 0.98 GB): 184 us,
-// 5.3 TB/s, 82% of the copy rate; 150 us with the products left out, and 185 us with all
-// weights in L2, so the computing warps bound it.  No single part holds them back (of 193 us
-// then: without the decode 180, the mma 195, the factors 182, the join 179): sixteen warps'
-// dependent steps per stage do.  Under the power cap of a long run (1.7 GHz) it takes 215 to
-// 220 us.  More warps with fewer registers, eight warps with
-// twice the rows, epilogue warps of their own, deeper or shallower rings and factors made a
-// stage ahead were all slower.
+// Measured (device time, gate_up of 64 tokens over 128 experts of 5760 x 2880, 0.98 GB): 202 to
+// 220 us in a steady run (about 1.7 GHz under the power cap), 183 us in a short burst, 5.3 TB/s, 82%
+// of the copy rate; in bursts also: 150 us with the products left out, and 185 us with all weights
+// in L2, so the computing warps bound it.  No single part holds them back (of 193 us then: without
+// the decode 180, the mma 195, the factors 182, the join 179): sixteen warps' dependent steps per
+// stage do.  More warps with fewer registers, eight warps with twice the rows, epilogue warps of
+// their own, deeper or shallower rings and factors made a stage ahead were all slower.  Long K with
+// several rows (8 rows of 28672 x 8192 50 us for 19 at the copy rate: x leaves room for the low tile
+// only) and more than 8 rows of one matrix (32 of 5760 x 2880 15 us for 1.4: decoded anew for every 8)
+// are furthest from it.
 #pragma once
 #include <type_traits>
 

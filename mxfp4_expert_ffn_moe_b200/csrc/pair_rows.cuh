@@ -22,11 +22,12 @@
 // the two ends of a tensor, which may not be its own, are read with plain loads.
 //
 // Measured (device time; share of the 6.55 TB/s copy rate): combine's gradient with the dots,
-// 8192 tokens x 4 x 2880 bf16, 76 us, 86%; combine, 4096 x 4 x 2880 bf16, 21 us, 84%; dispatch's
-// gradient with the dots, same sizes, 26 us, 84%; combine of fp32 rows 35 us, 93%; 4096 x 4 rows
-// of 1001 bf16 11 us, 57%.  With direct loads (four 16-byte ones in flight a thread) these took
-// 85, 23, 32, 35 and 18 us.  The spread without dots writes four times what it reads: 45 us
-// at 8192 tokens, 80%, by copies and by stores alike.
+// 8192 tokens x 4 x 2880 bf16, 76 us, 85%; combine, 4096 x 4 x 2880 bf16, 21 us, 84%; dispatch's
+// gradient with the dots, same sizes, 27 us, 79%; combine of fp32 rows 35 us, 92%; 4096 x 4 rows
+// of 1001 bf16: combine 11 us, 55%, dispatch 14 us, 45%, their gradients 18 and 15 us.  With direct
+// loads (four 16-byte ones in flight a thread) the first five took 85, 23, 32, 35 and 18 us.  The
+// spread without dots writes four times what it reads: 8192 tokens 45 us, 80%, by copies where no
+// weight is applied, 48 us, 75%, by stores.
 #pragma once
 #include <cuda_fp16.h>
 
