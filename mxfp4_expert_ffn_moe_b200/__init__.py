@@ -491,9 +491,12 @@ class _Call:
             raise ValueError(f"expected tensors on the current CUDA device, got one on {like.device}")
         self.side = None
         self.stream = torch._C._cuda_getCurrentRawStream(self.device)
-        if stream is not None and stream.cuda_stream != self.stream:
-            self.side = stream
-            self.stream = stream.cuda_stream
+        if stream is not None:
+            if stream.device_index != self.device:       # its handle may be 0, the current device's default stream
+                raise ValueError(f"expected a stream of cuda:{self.device}, got one of cuda:{stream.device_index}")
+            if stream.cuda_stream != self.stream:
+                self.side = stream
+                self.stream = stream.cuda_stream
 
     def empty(self, like, shape, dtype):
         # (empty_strided takes 1.5 us where new_empty takes 1.9 and empty 2.3)

@@ -52,3 +52,26 @@ def test_the_types_that_rows_may_have():
             call.rows(torch.zeros((3, 4), dtype=dtype), "x", 3, 4)
     with pytest.raises(ValueError, match="tensor of torch.float16"):
         call.rows(torch.zeros((3, 4)), "x", 3, 4, torch.float16)
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
+
+    class Tensor:
+        device = "cuda:0"
+
+        @staticmethod
+        def get_device():
+            return 0
+
+    class Stream:
+        def __init__(self, device_index, cuda_stream):
+            self.device_index, self.cuda_stream = device_index, cuda_stream
+
+    for handle in (0, 7):                                   # every device's default stream has the handle 0
+        with pytest.raises(ValueError, match="stream of cuda:0"):
+            moe._Call(Tensor, Stream(1, handle))
+    assert moe._Call(Tensor, Stream(0, 0)).side is None
+    assert moe._Call(Tensor, Stream(0, 7)).stream == 7
